@@ -10,6 +10,12 @@
  *   mamba_causal_conv1d_fwd       the block's causal conv1d + SiLU producing the scan's u
  *   mamba_causal_conv1d_update    its one-token decode step on a rolling conv state
  *   mamba_causal_conv1d_bwd       the gradients of that convolution (training)
+ *   mamba_gated_scan_fwd / _bwd   the gated linear recurrence and its gradients
+ *   mamba_gated_state_update      its one-token decode step
+ *   mamba_add_rms_norm_fwd / _fp8 / _bwd  the residual addition with RMS norm that opens a
+ *                                 block, its output in 8 bits with scales, its gradients
+ *   mamba_fp8_quantize            activations to 8 bits with a scale per 128 (_weight: blocks)
+ *   mamba_fp8_linear              the block's projections on such operands
  *
  * Definitions (Mamba: Linear-Time Sequence Modeling with Selective State Spaces,
  * page "xyznot.com/ar/paper/2312.00752", sections "Method", "Selection mechanism
@@ -72,6 +78,12 @@ typedef enum {
  * below, so the weight stays accurate as Delta A_n -> 0.
  */
 #define MAMBA_FLAG_EXACT_ZOH 1u
+
+/*
+ * MAMBA_FLAG_GIVEN_DECAY (the mamba_gated_* calls only): the gate tensor holds the decays
+ * a_t themselves and x enters unscaled.
+ */
+#define MAMBA_FLAG_GIVEN_DECAY 2u
 
 /* Problem sizes: batch >= 1, dim >= 1, 1 <= dstate <= 16, seqlen >= 0. */
 typedef struct {
@@ -454,6 +466,182 @@ int mamba_causal_conv1d_bwd(const void* x, const float* weight, const float* bia
                             float* dweight, float* dbias, void* dinitial_state, int64_t batch,
                             int64_t dim, int64_t seqlen, int width, int silu, mamba_dtype dtype,
                             void* stream);
+
+/*
+ * ---- The gated linear recurrence ------------------------------------------------------
+ *
+ * Per (batch, channel) row, with h_{-1} = initial_state (zero when NULL):
+ *
+ *   sigmoid form (flags = 0):  s_t = sigmoid(gate[t] + gate_bias[d]),
+ *                              h_t = (1 - s_t) h_{t-1} + s_t x[t]
+ *   MAMBA_FLAG_GIVEN_DECAY:    h_t = gate[t] h_{t-1} + x[t]       (gate_bias is not used)
+ *   y[t] = h_t * silu(z[t])    (y[t] = h_t when z is NULL)
+ *
+ * The sigmoid form is the gated RNN that the selective SSM reduces to with N = 1, A = -1,
+ * B = 1 (Mamba, section "Selection mechanism (S6)"); given decays cover other gates.  The
+ * kernels form products of up to seqlen decays, so given decays are expected in [-1, 1]
+ * (larger ones are right while no product of consecutive decays overflows fp32).
+ */
+typedef struct {
+    int64_t batch;
+    int64_t dim;
+    int64_t seqlen;
+} mamba_gated_dims; /* batch >= 1, dim >= 1, seqlen >= 0 */
+
+/*
+ * Bytes of workspace mamba_gated_scan_fwd needs (zero unless there are too few rows to
+ * occupy the GPU and each is cut into segments), of the checkpoints it can record, and of
+ * the workspace of mamba_gated_scan_bwd.  They depend on `dims` only; 0 for invalid dims.
+ */
+size_t mamba_gated_scan_workspace_size(mamba_gated_dims dims);
+size_t mamba_gated_scan_checkpoints_size(mamba_gated_dims dims);
+size_t mamba_gated_scan_bwd_workspace_size(mamba_gated_dims dims);
+
+/*
+ *   x, gate, z    : (batch, dim, seqlen) in_dtype      z may be NULL (no output gate)
+ *   gate_bias     : (dim) float32 or NULL
+ *   initial_state : (batch, dim) float32 or NULL
+ *   y             : (batch, dim, seqlen) out_dtype     written
+ *   last_state    : (batch, dim) float32 or NULL; receives h_{L-1} (the initial state when
+ *                   seqlen == 0)
+ *   checkpoints   : NULL, or checkpoint_bytes >= mamba_gated_scan_checkpoints_size(dims)
+ *                   bytes that receive the state entering every 256 steps, for the backward
+ *
+ * fp32 arithmetic and state.  Errors: NULL, DIMS, ALIGN, DTYPE, WORKSPACE, FLAGS, CUDA.
+ */
+int mamba_gated_scan_fwd(const void* x, const void* gate, const float* gate_bias, const void* z,
+                         const float* initial_state, void* y, float* last_state,
+                         float* checkpoints, size_t checkpoint_bytes, mamba_gated_dims dims,
+                         mamba_dtype in_dtype, mamba_dtype out_dtype, void* workspace,
+                         size_t workspace_bytes, unsigned flags, void* stream);
+
+/*
+ * Gradients of sum y dy + sum last_state dlast_state for mamba_gated_scan_fwd with the same
+ * inputs and flags.
+ *
+ *   dy             : (batch, dim, seqlen) dtype        gradient of y
+ *   dlast_state    : (batch, dim) float32 or NULL      gradient of last_state (NULL: zero)
+ *   dx, dgate      : (batch, dim, seqlen) dtype        written
+ *   dz             : (batch, dim, seqlen) dtype        written; NULL iff z is NULL
+ *   dgate_bias     : (dim) float32, written; NULL iff gate_bias is NULL or decays are given
+ *   dinitial_state : (batch, dim) float32 or NULL, written
+ *   checkpoints    : what mamba_gated_scan_fwd recorded for the same inputs, or NULL: the
+ *                    backward then forms them itself, with one more pass over x and gate
+ *   workspace      : at least mamba_gated_scan_bwd_workspace_size(dims) bytes
+ *
+ * No atomics: equal calls give equal bits.  With seqlen == 0, dinitial_state is dlast_state.
+ * Errors: as the forward.
+ */
+int mamba_gated_scan_bwd(const void* x, const void* gate, const float* gate_bias, const void* z,
+                         const float* initial_state, const void* dy, const float* dlast_state,
+                         void* dx, void* dgate, void* dz, float* dgate_bias,
+                         float* dinitial_state, const float* checkpoints, size_t checkpoint_bytes,
+                         mamba_gated_dims dims, mamba_dtype dtype, void* workspace,
+                         size_t workspace_bytes, unsigned flags, void* stream);
+
+/*
+ * One decode token of the recurrence, in place on state (batch, dim) float32;
+ * x, gate, z (or NULL), y: (batch, dim) dtype.  Errors: NULL, DIMS, ALIGN, DTYPE, FLAGS, CUDA.
+ */
+int mamba_gated_state_update(float* state, const void* x, const void* gate, const float* gate_bias,
+                             const void* z, void* y, int64_t batch, int64_t dim,
+                             mamba_dtype dtype, unsigned flags, void* stream);
+
+/*
+ * ---- Residual addition with RMS norm (the step that opens a block) ---------------------
+ *
+ *   v = residual + x (v = x when residual is NULL), rounded to residual_dtype
+ *   residual_out = v,   out = v / sqrt(mean(v^2) + eps) * weight
+ *
+ *   x            : (rows, dim) x_dtype
+ *   residual     : (rows, dim) residual_dtype or NULL (residual_dtype is then not used)
+ *   weight       : (dim) float32
+ *   out          : (rows, dim) out_dtype               written
+ *   residual_out : (rows, dim) residual_dtype          written; required with residual,
+ *                                                      else NULL or (rows, dim) x_dtype
+ *
+ * 1 <= dim <= 16384, rows >= 0; fp32 sums.  Errors: NULL, DIMS, ALIGN, DTYPE, CUDA.
+ */
+int mamba_add_rms_norm_fwd(const void* x, const void* residual, const float* weight, float eps,
+                           void* out, void* residual_out, int64_t rows, int64_t dim,
+                           mamba_dtype x_dtype, mamba_dtype residual_dtype, mamba_dtype out_dtype,
+                           void* stream);
+
+/*
+ * The same with the output in e4m3 and a scale for each row and 128 columns, as
+ * mamba_fp8_linear takes it: per group scale = max(largest |out|, 1e-30) / 448, q = out / scale
+ * rounded to nearest even.
+ *
+ *   q      : (rows, dim) e4m3                          dim a multiple of 16
+ *   scales : (rows, ceil(dim / 128)) float32
+ */
+int mamba_add_rms_norm_fp8(const void* x, const void* residual, const float* weight, float eps,
+                           void* q, float* scales, void* residual_out, int64_t rows, int64_t dim,
+                           mamba_dtype x_dtype, mamba_dtype residual_dtype, void* stream);
+
+/*
+ * Gradients of mamba_add_rms_norm_fwd, from its residual_out (x itself when the forward had
+ * no residual): with xhat = v / sqrt(mean(v^2) + eps) and g = dout * weight,
+ *   dv = dresidual_out + (g - xhat mean(g xhat)) / sqrt(mean(v^2) + eps)
+ *   dx = dresidual = dv,   dweight = sum over rows of dout * xhat
+ *
+ *   dout          : (rows, dim) x_dtype
+ *   residual_out  : (rows, dim) residual_dtype
+ *   dresidual_out : (rows, dim) residual_dtype or NULL (zero): the gradient that arrives at
+ *                   the residual stream from later blocks
+ *   dx            : (rows, dim) x_dtype                written
+ *   dresidual     : (rows, dim) residual_dtype or NULL, written (equal to dx but for rounding)
+ *   dweight       : (dim) float32                      written
+ *   workspace     : at least mamba_add_rms_norm_bwd_workspace_size(rows, dim) bytes
+ *
+ * No atomics: equal calls give equal bits.  Errors: NULL, DIMS, ALIGN, DTYPE, WORKSPACE, CUDA.
+ */
+size_t mamba_add_rms_norm_bwd_workspace_size(int64_t rows, int64_t dim);
+int mamba_add_rms_norm_bwd(const void* dout, const void* residual_out, const float* weight,
+                           const void* dresidual_out, float eps, void* dx, void* dresidual,
+                           float* dweight, int64_t rows, int64_t dim, mamba_dtype x_dtype,
+                           mamba_dtype residual_dtype, void* workspace, size_t workspace_bytes,
+                           void* stream);
+
+/*
+ * ---- 8-bit operands and the projections -------------------------------------------------
+ *
+ * Activations to e4m3, a scale for each token and 128 channels (scale and rounding as in
+ * mamba_add_rms_norm_fp8; NaN stays NaN, a group with an infinity has scale infinity).
+ *
+ *   x      : (batch * seqlen, dim) dtype, or (batch, dim, seqlen) when channel_major != 0 (the
+ *            layout of the scan's y: the call also transposes)
+ *   q      : (batch * seqlen, dim) e4m3                dim a multiple of 16
+ *   scales : (batch * seqlen, ceil(dim / 128)) float32
+ *
+ * Errors: NULL, DIMS, ALIGN, DTYPE, CUDA.
+ */
+int mamba_fp8_quantize(const void* x, void* q, float* scales, int64_t batch, int64_t dim,
+                       int64_t seqlen, int channel_major, mamba_dtype dtype, void* stream);
+
+/*
+ * Weights (n, k) to e4m3 (n, k), a scale for each block of 128 x 128: scales
+ * (ceil(n / 128), ceil(k / 128)) float32.  k a multiple of 16.
+ */
+int mamba_fp8_quantize_weight(const void* w, void* q, float* scales, int64_t n, int64_t k,
+                              mamba_dtype dtype, void* stream);
+
+/*
+ * The projection out[t, j] = sum_i (xq[t, i] x_scales[t, i / 128]) (wq[j, i] w_scales[j / 128,
+ * i / 128]) of operands quantised as above.
+ *
+ *   xq, x_scales : (tokens, k) e4m3, (tokens, ceil(k / 128)) float32
+ *   wq, w_scales : (n, k) e4m3, (ceil(n / 128), ceil(k / 128)) float32    k a multiple of 16
+ *   out          : (tokens, n) out_dtype when seqlen == 0; with seqlen > 0 (tokens a multiple of it)
+ *                  (tokens / seqlen, n, seqlen), the layout of the conv's and the scans' inputs
+ *
+ * Products are summed 128 inputs at a time by the tensor cores and the scaled sums in fp32.
+ * Errors: NULL, DIMS, ALIGN, DTYPE, CUDA; a bounded device wait that gave up is reported by
+ * mamba_check_device_error.
+ */
+int mamba_fp8_linear(const void* xq, const float* x_scales, const void* wq, const float* w_scales,
+                     void* out, int64_t tokens, int64_t n, int64_t k, int64_t seqlen,
+                     mamba_dtype out_dtype, void* stream);
 
 /*
  * Reads the library's device error word on `stream`, synchronising that stream.

@@ -6,6 +6,7 @@
 #include <stdint.h>
 
 #include "../../include/mamba_s6.h"
+#include "layer_launch.h"
 #include "s6_launch.h"
 
 namespace {
@@ -548,17 +549,18 @@ int mamba_diag_wait_timeout(int64_t limit_cycles, void* stream) {
 }
 
 int mamba_check_device_error(int clear, void* stream) {
-    unsigned word = 0;
-    if (s6::read_device_error(&word, clear != 0, static_cast<cudaStream_t>(stream)) != cudaSuccess)
+    unsigned word = 0, linear = 0;
+    if (s6::read_device_error(&word, clear != 0, static_cast<cudaStream_t>(stream)) != cudaSuccess ||
+        s6::read_linear_error(&linear, clear != 0, static_cast<cudaStream_t>(stream)) != cudaSuccess)
         return MAMBA_ERR_CUDA;
-    return word ? MAMBA_ERR_TIMEOUT : MAMBA_OK;
+    return word | linear ? MAMBA_ERR_TIMEOUT : MAMBA_OK;
 }
 
 const char* mamba_status_string(int status) {
     switch (status) {
         case MAMBA_OK: return "ok";
         case MAMBA_ERR_NULL: return "a required pointer is NULL";
-        case MAMBA_ERR_DIMS: return "invalid sizes (batch, dim >= 1; 1 <= dstate <= 16; seqlen >= 0)";
+        case MAMBA_ERR_DIMS: return "invalid sizes (the limits of each call are in mamba_s6.h)";
         case MAMBA_ERR_ALIGN: return "a pointer is not 16-byte aligned";
         case MAMBA_ERR_DTYPE: return "unknown dtype";
         case MAMBA_ERR_WORKSPACE: return "workspace missing or too small";
@@ -569,6 +571,6 @@ const char* mamba_status_string(int status) {
     }
 }
 
-int mamba_abi_version(void) { return 105; }
+int mamba_abi_version(void) { return 106; }
 
 }  // extern "C"

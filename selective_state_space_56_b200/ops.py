@@ -20,6 +20,7 @@ LIB_PATH = os.path.join(_HERE, "libmamba_s6.so")
 
 MAMBA_F32, MAMBA_BF16 = 0, 1
 MAMBA_FLAG_EXACT_ZOH = 1
+MAMBA_FLAG_GIVEN_DECAY = 2
 _DTYPES = {torch.float32: MAMBA_F32, torch.bfloat16: MAMBA_BF16}
 
 
@@ -32,6 +33,10 @@ class MambaError(RuntimeError):
 class ScanDims(ctypes.Structure):
     _fields_ = [("batch", ctypes.c_int64), ("dim", ctypes.c_int64), ("dstate", ctypes.c_int64),
                 ("seqlen", ctypes.c_int64)]
+
+
+class GatedDims(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int64), ("dim", ctypes.c_int64), ("seqlen", ctypes.c_int64)]
 
 
 _lock = threading.Lock()
@@ -99,6 +104,25 @@ def load_library():
             lib.mamba_selective_state_update.restype = i32
             lib.mamba_selective_state_update.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, vp, i32,
                                                          vp, i64, i64, i64, i32, vp]
+            size, f32 = ctypes.c_size_t, ctypes.c_float
+            for name in ("workspace", "checkpoints", "bwd_workspace"):
+                fn = getattr(lib, "mamba_gated_scan_%s_size" % name)
+                fn.restype, fn.argtypes = size, [GatedDims]
+            lib.mamba_add_rms_norm_bwd_workspace_size.restype = size
+            lib.mamba_add_rms_norm_bwd_workspace_size.argtypes = [i64, i64]
+            for name, args in (
+                    ("gated_scan_fwd", [vp] * 8 + [size, GatedDims, i32, i32, vp, size, u32, vp]),
+                    ("gated_scan_bwd", [vp] * 13 + [size, GatedDims, i32, vp, size, u32, vp]),
+                    ("gated_state_update", [vp] * 6 + [i64, i64, i32, u32, vp]),
+                    ("add_rms_norm_fwd", [vp] * 3 + [f32, vp, vp, i64, i64, i32, i32, i32, vp]),
+                    ("add_rms_norm_fp8", [vp] * 3 + [f32, vp, vp, vp, i64, i64, i32, i32, vp]),
+                    ("add_rms_norm_bwd", [vp] * 4 + [f32] + [vp] * 3 + [i64, i64, i32, i32, vp,
+                                                                        size, vp]),
+                    ("fp8_quantize", [vp] * 3 + [i64, i64, i64, i32, i32, vp]),
+                    ("fp8_quantize_weight", [vp] * 3 + [i64, i64, i32, vp]),
+                    ("fp8_linear", [vp] * 5 + [i64] * 4 + [i32, vp])):
+                fn = getattr(lib, "mamba_" + name)
+                fn.restype, fn.argtypes = i32, args
             lib.mamba_status_string.restype = ctypes.c_char_p
             lib.mamba_status_string.argtypes = [i32]
             lib.mamba_check_device_error.restype = i32
@@ -541,3 +565,306 @@ def selective_scan_fold(h_ends, delta_sums, A, h0=None, return_delta_sum=False):
     if rc != 0:
         raise MambaError(rc, "mamba_selective_scan_fold")
     return (h_out, s_out) if return_delta_sum else h_out
+
+
+# ---- The gated linear recurrence --------------------------------------------------------
+
+
+def _cuda_device(t, name, where, ndim):
+    if not isinstance(t, torch.Tensor) or t.dim() not in ndim:
+        raise ValueError("%s must be a tensor of %s dimensions" % (name, " or ".join(map(str, ndim))))
+    if t.device.type != "cuda":
+        raise ValueError("%s runs on CUDA tensors only" % where)
+    return t.device
+
+
+def _dtype(dt, what):
+    if dt not in _DTYPES:
+        raise ValueError("unsupported %s dtype %s" % (what, dt))
+    return _DTYPES[dt]
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _bytes(t):
+    return 0 if t is None else t.numel() * t.element_size()
+
+
+def _run(name, dev, *args):
+    """One library call on dev's current stream; raises MambaError for a non-zero status."""
+    fn = getattr(load_library(), name)
+    if dev.index == torch.cuda.current_device():
+        rc = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
+    else:
+        with torch.cuda.device(dev):
+            rc = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
+    if rc != 0:
+        raise MambaError(rc, name)
+
+
+def gated_scan_workspace_size(batch: int, dim: int, seqlen: int) -> int:
+    """Bytes of workspace ``gated_scan_fwd`` needs for these sizes (0 if none)."""
+    return int(load_library().mamba_gated_scan_workspace_size(GatedDims(batch, dim, seqlen)))
+
+
+def gated_scan_checkpoints_size(batch: int, dim: int, seqlen: int) -> int:
+    """Bytes of the checkpoints ``gated_scan_fwd`` can record for ``gated_scan_bwd``."""
+    return int(load_library().mamba_gated_scan_checkpoints_size(GatedDims(batch, dim, seqlen)))
+
+
+def gated_scan_bwd_workspace_size(batch: int, dim: int, seqlen: int) -> int:
+    """Bytes of workspace ``gated_scan_bwd`` needs for these sizes."""
+    return int(load_library().mamba_gated_scan_bwd_workspace_size(GatedDims(batch, dim, seqlen)))
+
+
+def _workspace(workspace, need, dev):
+    if need > 0 and workspace is None:
+        return torch.empty(need, dtype=torch.uint8, device=dev)
+    _check(workspace, "workspace", dev)
+    return workspace
+
+
+def gated_scan_fwd(x, gate, gate_bias=None, z=None, initial_state=None, given_decay=False,
+                   out_dtype=None, y=None, last_state=None, return_last_state=False,
+                   checkpoints=None, workspace=None):
+    """Gated linear recurrence h_t = (1 - s_t) h_{t-1} + s_t x_t with s_t = sigmoid(gate_t +
+    gate_bias), or h_t = gate_t h_{t-1} + x_t with given_decay; y_t = h_t silu(z_t) (h_t
+    without z).  x, gate, z: (batch, dim, L); gate_bias: (dim) fp32; initial_state: (batch,
+    dim) fp32 (zero when None).  Returns y (batch, dim, L) [and last_state (batch, dim) fp32].
+    checkpoints: a uint8 CUDA tensor of gated_scan_checkpoints_size(...) bytes to record what
+    ``gated_scan_bwd`` starts from."""
+    dev = _cuda_device(x, "x", "gated_scan_fwd", (3,))
+    b, d, L = x.shape
+    in_dt = x.dtype
+    out_dt = in_dt if out_dtype is None else out_dtype
+    in_code, out_code = _dtype(in_dt, "input"), _dtype(out_dt, "output")
+    f32 = (torch.float32,)
+    _check(x, "x", dev)
+    _check(gate, "gate", dev, (b, d, L), (in_dt,))
+    _check(z, "z", dev, (b, d, L), (in_dt,))
+    _check(gate_bias, "gate_bias", dev, (d,), f32)
+    _check(initial_state, "initial_state", dev, (b, d), f32)
+    if y is None:
+        y = torch.empty((b, d, L), dtype=out_dt, device=dev)
+    else:
+        _check(y, "y", dev, (b, d, L), (out_dt,))
+    if last_state is None and return_last_state:
+        last_state = torch.empty((b, d), dtype=torch.float32, device=dev)
+    _check(last_state, "last_state", dev, (b, d), f32)
+    _check(checkpoints, "checkpoints", dev)
+    dims = GatedDims(b, d, L)
+    workspace = _workspace(workspace, load_library().mamba_gated_scan_workspace_size(dims), dev)
+    _run("mamba_gated_scan_fwd", dev, x.data_ptr(), gate.data_ptr(), _addr(gate_bias), _addr(z),
+         _addr(initial_state), y.data_ptr(), _addr(last_state), _addr(checkpoints),
+         _bytes(checkpoints), dims, in_code, out_code, _addr(workspace), _bytes(workspace),
+         MAMBA_FLAG_GIVEN_DECAY if given_decay else 0)
+    return (y, last_state) if return_last_state else y
+
+
+def gated_scan_bwd(x, gate, dy, gate_bias=None, z=None, initial_state=None, dlast_state=None,
+                   given_decay=False, checkpoints=None, workspace=None):
+    """Gradients of sum(y dy) + sum(last_state dlast_state) for ``gated_scan_fwd`` with the
+    same inputs.  Returns a dict: dx, dgate, dz (batch, dim, L) in the inputs' dtype (dz None
+    without z), dgate_bias (dim) fp32 (None without a bias or with given_decay),
+    dinitial_state (batch, dim) fp32.  checkpoints: the buffer the forward filled for the same
+    inputs; without it the backward makes one more pass over x and gate."""
+    dev = _cuda_device(x, "x", "gated_scan_bwd", (3,))
+    b, d, L = x.shape
+    dt = x.dtype
+    code = _dtype(dt, "input")
+    f32 = (torch.float32,)
+    _check(x, "x", dev)
+    for t, name in ((gate, "gate"), (dy, "dy"), (z, "z")):
+        _check(t, name, dev, (b, d, L), (dt,))
+    _check(gate_bias, "gate_bias", dev, (d,), f32)
+    _check(initial_state, "initial_state", dev, (b, d), f32)
+    _check(dlast_state, "dlast_state", dev, (b, d), f32)
+    _check(checkpoints, "checkpoints", dev)
+    g = dict(dx=torch.empty_like(x), dgate=torch.empty_like(x),
+             dz=None if z is None else torch.empty_like(x),
+             dgate_bias=None if gate_bias is None or given_decay
+             else torch.empty(d, dtype=torch.float32, device=dev),
+             dinitial_state=torch.empty((b, d), dtype=torch.float32, device=dev))
+    dims = GatedDims(b, d, L)
+    workspace = _workspace(workspace, load_library().mamba_gated_scan_bwd_workspace_size(dims), dev)
+    _run("mamba_gated_scan_bwd", dev, x.data_ptr(), gate.data_ptr(), _addr(gate_bias), _addr(z),
+         _addr(initial_state), dy.data_ptr(), _addr(dlast_state), g["dx"].data_ptr(),
+         g["dgate"].data_ptr(), _addr(g["dz"]), _addr(g["dgate_bias"]),
+         g["dinitial_state"].data_ptr(), _addr(checkpoints), _bytes(checkpoints), dims, code,
+         _addr(workspace), _bytes(workspace), MAMBA_FLAG_GIVEN_DECAY if given_decay else 0)
+    return g
+
+
+def gated_state_update(state, x, gate, gate_bias=None, z=None, given_decay=False, y=None):
+    """One decode token of the gated recurrence, in place on ``state`` (batch, dim) fp32;
+    x, gate, z: (batch, dim).  Returns y (batch, dim)."""
+    dev = _cuda_device(state, "state", "gated_state_update", (2,))
+    b, d = shape = state.shape
+    dt = x.dtype
+    code = _dtype(dt, "input")
+    _check(state, "state", dev, shape, (torch.float32,))
+    _check(x, "x", dev, shape)
+    _check(gate, "gate", dev, shape, (dt,))
+    _check(z, "z", dev, shape, (dt,))
+    _check(gate_bias, "gate_bias", dev, (d,), (torch.float32,))
+    if y is None:
+        y = torch.empty_like(x)
+    else:
+        _check(y, "y", dev, shape, (dt,))
+    _run("mamba_gated_state_update", dev, state.data_ptr(), x.data_ptr(), gate.data_ptr(),
+         _addr(gate_bias), _addr(z), y.data_ptr(), b, d, code,
+         MAMBA_FLAG_GIVEN_DECAY if given_decay else 0)
+    return y
+
+
+# ---- Residual addition with RMS norm ----------------------------------------------------
+
+
+def _norm_inputs(x, weight, residual, residual_out, where):
+    dev = _cuda_device(x, "x", where, (2, 3))
+    d = x.shape[-1]
+    code = _dtype(x.dtype, "input")
+    _check(x, "x", dev)
+    _check(weight, "weight", dev, (d,), (torch.float32,))
+    rt = x.dtype
+    if residual is not None:
+        _check(residual, "residual", dev, x.shape)
+        rt = residual.dtype
+    rcode = _dtype(rt, "residual")
+    if residual_out is None:
+        residual_out = torch.empty_like(residual) if residual is not None else None
+    else:
+        _check(residual_out, "residual_out", dev, x.shape, (rt,))
+    return dev, d, code, rcode, residual_out
+
+
+def add_rms_norm_fwd(x, weight, residual=None, eps=1e-5, out_dtype=None, out=None,
+                     residual_out=None):
+    """v = residual + x (in the residual's dtype); out = v / sqrt(mean v^2 + eps) * weight.
+    x, residual: (..., dim) of 2 or 3 dimensions, weight: (dim) fp32.  Returns (out, v);
+    without a residual v is x."""
+    dev, d, code, rcode, residual_out = _norm_inputs(x, weight, residual, residual_out,
+                                                     "add_rms_norm_fwd")
+    out_dt = x.dtype if out_dtype is None else out_dtype
+    ocode = _dtype(out_dt, "output")
+    if out is None:
+        out = torch.empty(x.shape, dtype=out_dt, device=dev)
+    else:
+        _check(out, "out", dev, x.shape, (out_dt,))
+    _run("mamba_add_rms_norm_fwd", dev, x.data_ptr(), _addr(residual), weight.data_ptr(), eps,
+         out.data_ptr(), _addr(residual_out), x.numel() // d if d else 0, d, code, rcode, ocode)
+    return out, x if residual_out is None else residual_out
+
+
+def add_rms_norm_fp8(x, weight, residual=None, eps=1e-5, q=None, scales=None, residual_out=None):
+    """``add_rms_norm_fwd`` with the output in e4m3: returns (q (..., dim) float8_e4m3fn,
+    scales (..., ceil(dim / 128)) fp32, v), out = q * scale.  dim a multiple of 16."""
+    dev, d, code, rcode, residual_out = _norm_inputs(x, weight, residual, residual_out,
+                                                     "add_rms_norm_fp8")
+    lead = tuple(x.shape[:-1])
+    q, scales = _fp8_outputs(q, scales, lead, d, dev)
+    _run("mamba_add_rms_norm_fp8", dev, x.data_ptr(), _addr(residual), weight.data_ptr(), eps,
+         q.data_ptr(), scales.data_ptr(), _addr(residual_out), x.numel() // d if d else 0, d, code,
+         rcode)
+    return q, scales, x if residual_out is None else residual_out
+
+
+def _fp8_outputs(q, scales, lead, d, dev):
+    if q is None:
+        q = torch.empty(lead + (d,), dtype=torch.float8_e4m3fn, device=dev)
+    else:
+        _check(q, "q", dev, lead + (d,), (torch.float8_e4m3fn,))
+    groups = (d + 127) // 128
+    if scales is None:
+        scales = torch.empty(lead + (groups,), dtype=torch.float32, device=dev)
+    else:
+        _check(scales, "scales", dev, lead + (groups,), (torch.float32,))
+    return q, scales
+
+
+def add_rms_norm_bwd(dout, residual_out, weight, dresidual_out=None, eps=1e-5, workspace=None):
+    """Gradients of ``add_rms_norm_fwd`` from the v it returned.  dout: (..., dim) in x's
+    dtype; dresidual_out: the gradient arriving at v from elsewhere, in its dtype.  Returns a
+    dict: dx (dout's dtype), dresidual (v's dtype; the same tensor where the dtypes agree),
+    dweight (dim) fp32."""
+    dev = _cuda_device(dout, "dout", "add_rms_norm_bwd", (2, 3))
+    d = dout.shape[-1]
+    code = _dtype(dout.dtype, "input")
+    _check(dout, "dout", dev)
+    _check(residual_out, "residual_out", dev, dout.shape)
+    rt = residual_out.dtype
+    rcode = _dtype(rt, "residual")
+    _check(weight, "weight", dev, (d,), (torch.float32,))
+    _check(dresidual_out, "dresidual_out", dev, dout.shape, (rt,))
+    dx = torch.empty_like(dout)
+    dres = None if rt == dout.dtype else torch.empty_like(residual_out)
+    dw = torch.empty(d, dtype=torch.float32, device=dev)
+    rows = dout.numel() // d if d else 0
+    workspace = _workspace(workspace, load_library().mamba_add_rms_norm_bwd_workspace_size(rows, d),
+                           dev)
+    _run("mamba_add_rms_norm_bwd", dev, dout.data_ptr(), residual_out.data_ptr(), weight.data_ptr(),
+         _addr(dresidual_out), eps, dx.data_ptr(), _addr(dres), dw.data_ptr(), rows, d, code, rcode,
+         _addr(workspace), _bytes(workspace))
+    return dict(dx=dx, dresidual=dx if dres is None else dres, dweight=dw)
+
+
+# ---- 8-bit operands and the projections -------------------------------------------------
+
+
+def fp8_quantize(x, channel_major=False, q=None, scales=None):
+    """Activations to e4m3 with a scale for each token and 128 channels: x (tokens, dim), or
+    (batch, dim, L) with channel_major (the layout of the scans' y).  Returns (q (tokens, dim)
+    float8_e4m3fn, scales (tokens, ceil(dim / 128)) fp32), tokens = batch * L in the latter
+    case.  dim a multiple of 16."""
+    dev = _cuda_device(x, "x", "fp8_quantize", (3,) if channel_major else (2,))
+    code = _dtype(x.dtype, "input")
+    _check(x, "x", dev)
+    b, d, L = x.shape if channel_major else (1, x.shape[1], x.shape[0])
+    q, scales = _fp8_outputs(q, scales, (b * L,), d, dev)
+    _run("mamba_fp8_quantize", dev, x.data_ptr(), q.data_ptr(), scales.data_ptr(), b, d, L,
+         int(bool(channel_major)), code)
+    return q, scales
+
+
+def fp8_quantize_weight(w):
+    """Weights (n, k) to e4m3 with a scale for each block of 128 x 128: returns (q (n, k)
+    float8_e4m3fn, scales (ceil(n / 128), ceil(k / 128)) fp32).  k a multiple of 16."""
+    dev = _cuda_device(w, "w", "fp8_quantize_weight", (2,))
+    code = _dtype(w.dtype, "input")
+    _check(w, "w", dev)
+    n, k = w.shape
+    q = torch.empty((n, k), dtype=torch.float8_e4m3fn, device=dev)
+    scales = torch.empty(((n + 127) // 128, (k + 127) // 128), dtype=torch.float32, device=dev)
+    _run("mamba_fp8_quantize_weight", dev, w.data_ptr(), q.data_ptr(), scales.data_ptr(), n, k, code)
+    return q, scales
+
+
+def fp8_linear(xq, x_scales, wq, w_scales, out_dtype=torch.bfloat16, channel_major_seqlen=None,
+               out=None):
+    """The projection x w^T of operands in e4m3 (``fp8_quantize`` / ``add_rms_norm_fp8`` and
+    ``fp8_quantize_weight``): xq (tokens, k), wq (n, k).  Returns (tokens, n), or with
+    channel_major_seqlen = L the layout of the conv's and the scans' inputs, (tokens / L, n, L)."""
+    dev = _cuda_device(xq, "xq", "fp8_linear", (2,))
+    code = _dtype(out_dtype, "output")
+    t, k = xq.shape
+    n = wq.shape[0] if isinstance(wq, torch.Tensor) and wq.dim() == 2 else -1
+    f8, f32, kb = (torch.float8_e4m3fn,), (torch.float32,), (k + 127) // 128
+    _check(xq, "xq", dev, None, f8)
+    _check(x_scales, "x_scales", dev, (t, kb), f32)
+    _check(wq, "wq", dev, (n, k), f8)
+    _check(w_scales, "w_scales", dev, ((n + 127) // 128, kb), f32)
+    L = 0
+    if channel_major_seqlen is not None:
+        L = int(channel_major_seqlen)
+        if L < 1 or t % L != 0:
+            raise ValueError("channel_major_seqlen must be positive and divide the %d tokens" % t)
+    shape = (t, n) if L == 0 else (t // L, n, L)
+    if out is None:
+        out = torch.empty(shape, dtype=out_dtype, device=dev)
+    else:
+        _check(out, "out", dev, shape, (out_dtype,))
+    _run("mamba_fp8_linear", dev, xq.data_ptr(), x_scales.data_ptr(), wq.data_ptr(),
+         w_scales.data_ptr(), out.data_ptr(), t, n, k, L, code)
+    return out
