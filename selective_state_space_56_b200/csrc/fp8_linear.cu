@@ -10,8 +10,10 @@
 // k and rows past the arrays arrive as zeros.
 //
 // Two kernels:
-//   prefill_kernel   128 tokens (the MMA's rows) x 256 outputs per tile, persistent CTAs.  A
-//                    lane is a token, so its scale is one register a block.
+//   prefill_kernel   256 tokens (the MMA's rows) x 256 outputs per tile, on persistent pairs of
+//                    CTAs (cta_group::2): each loads half of either operand, which halves the
+//                    weights' share of the shared-memory traffic that a 128 x 256 tile of one CTA is
+//                    bound by.  A lane is a token, so its scale is one register a block.
 //   token_kernel     few tokens: bound by the weights' bytes.  128 outputs are the MMA's rows,
 //                    the tokens its columns (16 to 128), and the inputs are cut into pieces over a
 //                    cluster whose CTAs add their sums through distributed shared memory in
@@ -101,6 +103,93 @@ __device__ __forceinline__ void mma_f8(uint32_t d, uint64_t a, uint64_t b, uint3
         "r"(idesc), "r"((uint32_t)add)
         : "memory");
 }
+// The same on a pair of CTAs (ranks 2i and 2i + 1 of a cluster): the leader (even rank) issues
+// products of 256 rows, 128 from each CTA's shared memory, and 256 columns, 128 from each; each
+// CTA's tensor memory receives its own 128 rows.
+__device__ __forceinline__ void tmem_alloc_pair(uint32_t* slot, uint32_t cols) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(slot)),
+                 "r"(cols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_free_pair(uint32_t addr, uint32_t cols) {
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(addr), "r"(cols) : "memory");
+}
+// Arrives at the barrier at this offset in both CTAs once the leader's products are done.
+__device__ __forceinline__ void tc_commit_pair(uint64_t* bar) {
+    asm volatile(
+        "{\n .reg .b16 m;\n mov.b16 m, 3;\n"
+        " tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], m;\n}\n" ::
+            "r"(smem_addr(bar))
+        : "memory");
+}
+__device__ __forceinline__ void mma_f8_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n"
+        " tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n}\n" ::"r"(d), "l"(a), "l"(b),
+        "r"(idesc), "r"((uint32_t)add)
+        : "memory");
+}
+// Shared-cluster address of a variable in the CTA of `rank`.
+__device__ __forceinline__ uint32_t peer_addr(const void* local, uint32_t rank) {
+    uint32_t a;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_addr(local)), "r"(rank));
+    return a;
+}
+// A load into this CTA's shared memory that completes on the pair leader's barrier.
+__device__ __forceinline__ void tma_load_2d_pair(void* dst, const CUtensorMap* map, int c0, int c1,
+                                                 uint32_t leader_bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3}], [%4];" ::"r"(smem_addr(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(leader_bar)
+        : "memory");
+}
+// An arrival at a barrier of the pair.  What it hands over is tensor memory, ordered by the
+// tcgen05 fences; releasing at cluster scope would make the warp wait for all its memory accesses
+// (that wait alone took two thirds of the kernel's time).
+__device__ __forceinline__ void arrive_at(uint32_t cluster_bar) {
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
+}
+template <int R>
+__device__ __forceinline__ void set_registers_up() {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R));
+}
+template <int R>
+__device__ __forceinline__ void set_registers_down() {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R));
+}
+
+// 32 lanes x 32 columns; valid after tmem_ld_wait.
+__device__ __forceinline__ void tmem_ld32(uint32_t addr, uint32_t (&r)[32]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, "
+        "%12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, "
+        "%30, %31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+          "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]),
+          "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]),
+          "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(addr));
+}
+// Uses of r stay behind this point (the registers pass through it).
+__device__ __forceinline__ void pin32(uint32_t (&r)[32]) {
+    asm volatile(""
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]),
+                   "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]),
+                   "+r"(r[13]), "+r"(r[14]), "+r"(r[15]), "+r"(r[16]), "+r"(r[17]), "+r"(r[18]),
+                   "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]), "+r"(r[24]),
+                   "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]),
+                   "+r"(r[31])::"memory");
+}
+// Waits for both loads; the registers pass through, so no use of them can be moved before it.
+__device__ __forceinline__ void tmem_ld_wait(uint32_t (&a)[32], uint32_t (&b)[32]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+    pin32(a);
+    pin32(b);
+}
+
 // 32 lanes x 16 columns of fp32 accumulators; the values are valid after tmem_ld_wait(r).
 __device__ __forceinline__ void tmem_ld16(uint32_t addr, uint32_t (&r)[16]) {
     asm volatile(
@@ -153,24 +242,68 @@ __device__ __forceinline__ int64_t out_index(const LParams& p, int64_t t, int64_
     return (b * p.n + n) * p.seqlen + (t - b * p.seqlen);
 }
 
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.aligned;\nbarrier.cluster.wait.aligned;" ::: "memory");
+}
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+
 // ---- Many tokens -----------------------------------------------------------------------
 
-constexpr int kPN = 256;      // outputs per tile
-constexpr int kPStages = 4;   // 4 x 48 KB
+constexpr int kPN = 256;                // outputs per tile
+constexpr int kPT = 2 * kBM;             // tokens per tile of a pair of CTAs
+constexpr int kPStages = 5;              // 5 x 32 KB a CTA
 constexpr int kPThreads = 384;
-constexpr uint32_t kPStageBytes = (kBM + kPN) * kBK;
-constexpr uint32_t kPSmem = kPStages * kPStageBytes + 1024;
+constexpr int kPWarps = 8;               // warps that keep the sums
+constexpr uint32_t kPStageBytes = 2 * kBM * kBK;  // 128 tokens and 128 weight rows
+constexpr uint32_t kPStaging = 8192;     // bytes of output a warp gathers before it stores
+constexpr uint32_t kPSmem = kPStages * kPStageBytes + kPWarps * kPStaging + 1024;
 
 struct PBars {
-    uint64_t full[kPStages], empty[kPStages];  // operand ring
-    uint64_t done[2], free[2];                 // accumulators: filled / read back
+    uint64_t full[kPStages], empty[kPStages];  // operand ring (full: the leader's counts for both)
+    uint64_t done[2], free[2];                 // accumulators: filled / read back (free: leader's)
     uint64_t drain;
     uint32_t tmem;
     Ctl ctl;
 };
 
-// Warp 0 loads, warp 1 issues the products, warp 2 owns tensor memory; warps 4-11 keep the
-// sums: warp w holds lanes (w % 4) * 32 .. and columns ((w - 4) / 4) * 128 .., 128 sums a thread.
+// Stores 32 rows (a lane each, rows `row_stride` apart, valid where `rows` says) x 64 bytes * 4 of
+// output through the warp's staging memory, so that a store covers whole lines: each lane
+// writes its row in pieces of 16 bytes, piece c at place c ^ (row % 16), and the warp then
+// reads two rows at a time.
+template <typename Tout>
+__device__ __forceinline__ void store_rows(uint8_t* stage, Tout* out, int64_t row_stride, int rows, int lane,
+                                           const f2* acc) {
+    constexpr int kPer = 16 / sizeof(Tout);  // outputs per piece; 16 pieces a row
+#pragma unroll
+    for (int c = 0; c < 16; ++c) {
+        alignas(16) Tout v[kPer];
+#pragma unroll
+        for (int j = 0; j < kPer / 2; ++j) {
+            float lo, hi;
+            unpack2(acc[c * (kPer / 2) + j], lo, hi);
+            v[2 * j] = io<Tout>::from_f(lo), v[2 * j + 1] = io<Tout>::from_f(hi);
+        }
+        *reinterpret_cast<uint4*>(stage + lane * 256 + ((c ^ (lane & 15)) * 16)) = *reinterpret_cast<uint4*>(v);
+    }
+    __syncwarp();
+    const int c = lane & 15;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        const int r = 2 * i + (lane >> 4);
+        const uint4 v = *reinterpret_cast<const uint4*>(stage + r * 256 + ((c ^ (r & 15)) * 16));
+        if (r < rows) *reinterpret_cast<uint4*>(out + (int64_t)r * row_stride + c * kPer) = v;
+    }
+    __syncwarp();
+}
+
+// A pair of CTAs per tile.  In each, warp 0 loads (its 128 tokens and its half of the weight
+// rows), warp 1 of the leader issues the products, warp 2 owns tensor memory; warps 4-11 keep the
+// sums of the CTA's tokens: warp w holds lanes (w % 4) * 32 .. and columns ((w - 4) / 4) * 128 ..,
+// 128 sums a thread.
 template <typename Tout>
 __global__ void __launch_bounds__(kPThreads, 1)
 prefill_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUtensorMap mw,
@@ -180,119 +313,134 @@ prefill_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ C
     uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(dyn) + 1023) & ~(uintptr_t)1023);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int tiles = p.tiles_t * p.tiles_n;
+    const uint32_t rank = cluster_rank();
+    const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
     if (threadIdx.x == 0) {
         for (int i = 0; i < kPStages; ++i) mbar_init(&bars.full[i], 1), mbar_init(&bars.empty[i], 1);
-        for (int i = 0; i < 2; ++i) mbar_init(&bars.done[i], 1), mbar_init(&bars.free[i], 8);
+        for (int i = 0; i < 2; ++i) mbar_init(&bars.done[i], 1), mbar_init(&bars.free[i], 2 * kPWarps);
         mbar_init(&bars.drain, 1);
         bars.ctl.abort = 0;
         fence_barrier_init();
     }
-    if (warp == 2) tmem_alloc(&bars.tmem, 512);
+    if (warp == 2) tmem_alloc_pair(&bars.tmem, 512);
     tc_fence_before();
     __syncthreads();
+    cluster_sync();  // both CTAs' barriers are set up
     tc_fence_after();
     const uint32_t tmem = bars.tmem;
 
-    if (warp == 0) {
-        if (elect_one()) {
-            int64_t it = 0;
-            bool ok = true;
-            for (int tile = blockIdx.x; tile < tiles && ok; tile += gridDim.x) {
-                const int tt = tile / p.tiles_n, tn = tile - tt * p.tiles_n;
-                for (int k = 0; k < p.kb; ++k, ++it) {
-                    const int s = (int)(it % kPStages);
-                    if (!wait_or_abort(&bars.empty[s], (uint32_t)((it / kPStages) & 1) ^ 1u, &bars.ctl)) {
-                        ok = false;
-                        break;
+    if (warp < 4) {
+        set_registers_down<56>();
+        if (warp == 0) {
+            if (elect_one()) {
+                int64_t it = 0;
+                bool ok = true;
+                for (int tile = pair; tile < tiles && ok; tile += pairs) {
+                    const int tt = tile / p.tiles_n, tn = tile - tt * p.tiles_n;
+                    for (int k = 0; k < p.kb; ++k, ++it) {
+                        const int s = (int)(it % kPStages);
+                        if (!wait_or_abort(&bars.empty[s], (uint32_t)((it / kPStages) & 1) ^ 1u, &bars.ctl)) {
+                            ok = false;
+                            break;
+                        }
+                        uint8_t* st = ring + s * kPStageBytes;
+                        const uint32_t full = peer_addr(&bars.full[s], 0);
+                        if (rank == 0) mbar_arrive_expect_tx(&bars.full[s], 2 * kPStageBytes);
+                        tma_load_2d_pair(st, &mx, k * kBK, tt * kPT + (int)rank * kBM, full);
+                        tma_load_2d_pair(st + kBM * kBK, &mw, k * kBK, tn * kPN + (int)rank * kBM, full);
                     }
-                    uint8_t* st = ring + s * kPStageBytes;
-                    mbar_arrive_expect_tx(&bars.full[s], kPStageBytes);
-                    tma_load_2d(st, &mx, k * kBK, tt * kBM, &bars.full[s]);
-                    tma_load_2d(st + kBM * kBK, &mw, k * kBK, tn * kPN, &bars.full[s]);
+                }
+                if (!ok && rank == 0)  // copies in flight (the last use of each stage) before the end
+                    for (int64_t j = it > kPStages ? it - kPStages : 0; j < it; ++j)
+                        mbar_wait_bounded(&bars.full[j % kPStages], (uint32_t)((j / kPStages) & 1), kLimit / 8);
+            }
+        } else if (warp == 1 && rank == 0) {
+            if (elect_one()) {
+                constexpr uint32_t idesc = mma_desc(kPT, kPN);
+                int64_t it = 0;
+                bool ok = true;
+                for (int tile = pair; tile < tiles && ok; tile += pairs) {
+                    for (int k = 0; k < p.kb; ++k, ++it) {
+                        const int s = (int)(it % kPStages), d = (int)(it & 1);
+                        if (!wait_or_abort(&bars.free[d], (uint32_t)((it >> 1) & 1) ^ 1u, &bars.ctl) ||
+                            !wait_or_abort(&bars.full[s], (uint32_t)((it / kPStages) & 1), &bars.ctl)) {
+                            ok = false;
+                            break;
+                        }
+                        tc_fence_after();
+                        const uint32_t a = smem_addr(ring + s * kPStageBytes);
+                        const uint64_t da = tile_desc(a), db = tile_desc(a + kBM * kBK);
+#pragma unroll
+                        for (int i = 0; i < kBK / 32; ++i)
+                            mma_f8_pair(tmem + d * kPN, da + i * 2, db + i * 2, idesc, i > 0);
+                        tc_commit_pair(&bars.empty[s]);
+                        tc_commit_pair(&bars.done[d]);
+                    }
+                }
+                if (!ok) {
+                    tc_commit_pair(&bars.drain);
+                    mbar_wait_bounded(&bars.drain, 0, kLimit / 8);
                 }
             }
-            if (!ok)  // copies in flight (the last use of each stage), before the CTA may end
-                for (int64_t j = it > kPStages ? it - kPStages : 0; j < it; ++j)
-                    mbar_wait_bounded(&bars.full[j % kPStages], (uint32_t)((j / kPStages) & 1), kLimit / 8);
         }
-    } else if (warp == 1) {
-        if (elect_one()) {
-            constexpr uint32_t idesc = mma_desc(kBM, kPN);
-            int64_t it = 0;
-            bool ok = true;
-            for (int tile = blockIdx.x; tile < tiles && ok; tile += gridDim.x) {
-                for (int k = 0; k < p.kb; ++k, ++it) {
-                    const int s = (int)(it % kPStages), d = (int)(it & 1);
-                    if (!wait_or_abort(&bars.free[d], (uint32_t)((it >> 1) & 1) ^ 1u, &bars.ctl) ||
-                        !wait_or_abort(&bars.full[s], (uint32_t)((it / kPStages) & 1), &bars.ctl)) {
-                        ok = false;
-                        break;
-                    }
-                    tc_fence_after();
-                    const uint32_t a = smem_addr(ring + s * kPStageBytes);
-                    mma_stage(tmem + d * kPN, a, a + kBM * kBK, idesc);
-                    tc_commit(&bars.empty[s]);
-                    tc_commit(&bars.done[d]);
-                }
-            }
-            if (!ok) {
-                tc_commit(&bars.drain);
-                mbar_wait_bounded(&bars.drain, 0, kLimit / 8);
-            }
-        }
-    } else if (warp >= 4) {
+    } else {
+        set_registers_up<224>();
         const int half = (warp - 4) >> 2, quad = warp & 3;
         const uint32_t base = tmem + ((uint32_t)(quad * 32) << 16) + half * 128;
+        uint8_t* stage = ring + kPStages * kPStageBytes + (warp - 4) * kPStaging;
+        const uint32_t free0 = peer_addr(&bars.free[0], 0), free1 = peer_addr(&bars.free[1], 0);
         int64_t it = 0;
         bool ok = true;
-        for (int tile = blockIdx.x; tile < tiles && ok; tile += gridDim.x) {
+        for (int tile = pair; tile < tiles && ok; tile += pairs) {
             const int tt = tile / p.tiles_n, tn = tile - tt * p.tiles_n;
-            const int64_t t = (int64_t)tt * kBM + quad * 32 + lane;
-            const int64_t n0 = (int64_t)tn * kPN + half * 128;
+            const int64_t t0 = (int64_t)tt * kPT + rank * kBM + quad * 32;  // the warp's first token
+            const int64_t t = t0 + lane, n0 = (int64_t)tn * kPN + half * 128;
             const bool in = t < p.tokens && n0 < p.n;
             const float* xs = p.xs + (in ? t : 0) * p.kb;
             const float* ws = p.ws + (in ? n0 / kGroup : 0) * p.kb;
             f2 acc[64];
 #pragma unroll
             for (int i = 0; i < 64; ++i) acc[i] = pack2(0.f, 0.f);
-            float sc = __ldg(xs) * __ldg(ws);
+            float xn = __ldg(xs), wn = __ldg(ws);
             for (int k = 0; k < p.kb; ++k, ++it) {
                 const int d = (int)(it & 1);
-                const int kn = k + 1 < p.kb ? k + 1 : k;
-                const float next = __ldg(xs + kn) * __ldg(ws + kn);
+                const float sc = xn * wn;
+                if (k + 1 < p.kb) xn = __ldg(xs + k + 1), wn = __ldg(ws + k + 1);  // used a block later
                 ok = __all_sync(kFull, wait_or_abort(&bars.done[d], (uint32_t)((it >> 1) & 1), &bars.ctl));
                 if (!ok) break;
                 tc_fence_after();
                 const f2 s2 = pack2(sc, sc);
 #pragma unroll
-                for (int c = 0; c < 8; ++c) {
-                    uint32_t r[16];
-                    tmem_ld16(base + d * kPN + c * 16, r);
-                    tmem_ld_wait(r);
+                for (int c = 0; c < 2; ++c) {
+                    uint32_t r0[32], r1[32];
+                    tmem_ld32(base + d * kPN + c * 64, r0);
+                    tmem_ld32(base + d * kPN + c * 64 + 32, r1);
+                    tmem_ld_wait(r0, r1);
+                    if (c == 1) {  // the accumulator is in registers: the next products may overwrite it
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) arrive_at(d ? free1 : free0);
+                    }
 #pragma unroll
-                    for (int j = 0; j < 8; ++j)
-                        acc[c * 8 + j] = fma2(pack2(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1])),
-                                              s2, acc[c * 8 + j]);
+                    for (int j = 0; j < 16; ++j) {
+                        acc[c * 32 + j] = fma2(pack2(__uint_as_float(r0[2 * j]), __uint_as_float(r0[2 * j + 1])), s2,
+                                               acc[c * 32 + j]);
+                        acc[c * 32 + 16 + j] = fma2(
+                            pack2(__uint_as_float(r1[2 * j]), __uint_as_float(r1[2 * j + 1])), s2, acc[c * 32 + 16 + j]);
+                    }
                 }
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&bars.free[d]);
-                sc = next;
             }
             if (!ok) break;
-            if (!in) continue;
             Tout* out = static_cast<Tout*>(p.out);
+            const int rows = (int)max((int64_t)0, min((int64_t)32, p.tokens - t0));
+            if (n0 >= p.n || rows == 0) continue;
             if (p.seqlen == 0) {
-                Tout* o = out + t * p.n + n0;
                 if (n0 + 128 <= p.n && p.n % 8 == 0) {
-#pragma unroll
-                    for (int c = 0; c < 16; ++c) {
-                        float v[kE];
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) unpack2(acc[c * 4 + j], v[2 * j], v[2 * j + 1]);
-                        store_all(o + c * kE, v);
-                    }
-                } else {
+                    Tout* o = out + t0 * p.n + n0;
+                    store_rows<Tout>(stage, o, p.n, rows, lane, acc);
+                    if (sizeof(Tout) == 4) store_rows<Tout>(stage, o + 64, p.n, rows, lane, acc + 32);
+                } else if (lane < rows) {
+                    Tout* o = out + t * p.n + n0;
 #pragma unroll
                     for (int c = 0; c < 64; ++c) {
                         float v0, v1;
@@ -301,7 +449,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ C
                         if (n0 + 2 * c + 1 < p.n) o[2 * c + 1] = io<Tout>::from_f(v1);
                     }
                 }
-            } else {
+            } else if (lane < rows) {
                 Tout* o = out + out_index<Tout>(p, t, n0);
 #pragma unroll
                 for (int c = 0; c < 64; ++c) {
@@ -315,8 +463,9 @@ prefill_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ C
     }
     tc_fence_before();
     __syncthreads();
+    cluster_sync();  // neither CTA ends while the other may still signal it or read its memory
     tc_fence_after();
-    if (warp == 2) tmem_free(tmem, 512);
+    if (warp == 2) tmem_free_pair(tmem, 512);
 }
 
 // ---- Few tokens ------------------------------------------------------------------------
@@ -334,19 +483,9 @@ struct TBars {
 template <int BN>
 constexpr uint32_t token_stage_bytes() { return (kBM + BN) * kBK; }
 
-__device__ __forceinline__ void cluster_sync() {
-    asm volatile("barrier.cluster.arrive.aligned;\nbarrier.cluster.wait.aligned;" ::: "memory");
-}
-__device__ __forceinline__ uint32_t cluster_rank() {
-    uint32_t r;
-    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-    return r;
-}
 __device__ __forceinline__ float peer_load(const float* local, uint32_t rank) {
-    uint32_t a;
     float v;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_addr(local)), "r"(rank));
-    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(a) : "memory");
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(peer_addr(local, rank)) : "memory");
     return v;
 }
 
@@ -523,15 +662,26 @@ int multiprocessors() {
 template <typename Tout>
 cudaError_t run_prefill(const LinearArgs& a, LParams p, cudaStream_t s) {
     CUtensorMap mx, mw;
-    if (!encode_rows(&mx, a.xq, a.k, a.tokens, kBM) || !encode_rows(&mw, a.wq, a.k, a.n, kPN))
+    if (!encode_rows(&mx, a.xq, a.k, a.tokens, kBM) || !encode_rows(&mw, a.wq, a.k, a.n, kBM))
         return cudaErrorInvalidValue;
-    p.tiles_t = (int)((a.tokens + kBM - 1) / kBM);
+    p.tiles_t = (int)((a.tokens + kPT - 1) / kPT);
     p.tiles_n = (int)((a.n + kPN - 1) / kPN);
     cudaError_t e = cudaFuncSetAttribute(prefill_kernel<Tout>, cudaFuncAttributeMaxDynamicSharedMemorySize, kPSmem);
     if (e != cudaSuccess) return e;
-    const int grid = (int)std::min<int64_t>((int64_t)p.tiles_t * p.tiles_n, multiprocessors());
-    prefill_kernel<Tout><<<grid, kPThreads, kPSmem, s>>>(mx, mw, p);
-    return cudaGetLastError();
+    const int64_t pairs = std::min<int64_t>((int64_t)p.tiles_t * p.tiles_n, std::max(1, multiprocessors() / 2));
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(2 * pairs));
+    cfg.blockDim = dim3(kPThreads);
+    cfg.dynamicSmemBytes = kPSmem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, prefill_kernel<Tout>, mx, mw, p);
 }
 
 template <int BN, typename Tout>
@@ -583,8 +733,8 @@ cudaError_t run_linear(const LinearArgs& a, cudaStream_t s) {
     p.seqlen = a.seqlen;
     p.kb = (int)((a.k + kBK - 1) / kBK);
     p.tiles_t = p.tiles_n = 0;
-    const int64_t big = ((a.tokens + kBM - 1) / kBM) * ((a.n + kPN - 1) / kPN);
-    if (big >= multiprocessors()) return run_prefill<Tout>(a, p, s);
+    const int64_t big = ((a.tokens + kPT - 1) / kPT) * ((a.n + kPN - 1) / kPN);
+    if (big >= multiprocessors() / 2) return run_prefill<Tout>(a, p, s);
     if (a.tokens <= 16) return run_token<16, Tout>(a, p, s);
     if (a.tokens <= 32) return run_token<32, Tout>(a, p, s);
     return run_token<64, Tout>(a, p, s);
