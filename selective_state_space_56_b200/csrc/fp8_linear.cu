@@ -183,11 +183,24 @@ __device__ __forceinline__ void pin32(uint32_t (&r)[32]) {
                    "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]),
                    "+r"(r[31])::"memory");
 }
-// Waits for both loads; the registers pass through, so no use of them can be moved before it.
-__device__ __forceinline__ void tmem_ld_wait(uint32_t (&a)[32], uint32_t (&b)[32]) {
+// The registers pass through the wait, so no use of them can be moved before it.
+__device__ __forceinline__ void tmem_ld_wait(uint32_t (&r)[32]) {
     asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-    pin32(a);
-    pin32(b);
+    pin32(r);
+}
+// acc += r * scale on 32 columns.  (Packed pairs cost two moves each: the loaded registers do not
+// arrive as pairs.)
+__device__ __forceinline__ void add_scaled(float* acc, const uint32_t (&r)[32], float scale) {
+#pragma unroll
+    for (int j = 0; j < 32; ++j) acc[j] = fmaf(__uint_as_float(r[j]), scale, acc[j]);
+}
+
+// Tiled store shared -> global; what lies outside the tensor is not written.
+__device__ __forceinline__ void tma_store_2d(const CUtensorMap* map, const void* src, int c0, int c1) {
+    asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%2, %3}], [%1];" ::"l"(
+                     reinterpret_cast<uint64_t>(map)),
+                 "r"(smem_addr(src)), "r"(c0), "r"(c1)
+                 : "memory");
 }
 
 // 32 lanes x 16 columns of fp32 accumulators; the values are valid after tmem_ld_wait(r).
@@ -233,6 +246,7 @@ struct LParams {
     int64_t tokens, n, seqlen;  // seqlen 0: token-major output
     int kb;                     // blocks of 128 inputs
     int tiles_t, tiles_n;
+    int out_tma;  // the output's rows can be described to TMA (16-byte multiples)
 };
 
 template <typename Tout>
@@ -256,11 +270,16 @@ __device__ __forceinline__ uint32_t cluster_rank() {
 constexpr int kPN = 256;                // outputs per tile
 constexpr int kPT = 2 * kBM;             // tokens per tile of a pair of CTAs
 constexpr int kPStages = 5;              // 5 x 32 KB a CTA
-constexpr int kPThreads = 384;
-constexpr int kPWarps = 8;               // warps that keep the sums
+constexpr int kPWarps = 8;               // warps that keep the sums, 32 tokens x 128 outputs each
+constexpr int kPCols = 128;
+constexpr int kPThreads = 128 + 32 * kPWarps;
 constexpr uint32_t kPStageBytes = 2 * kBM * kBK;  // 128 tokens and 128 weight rows
-constexpr uint32_t kPStaging = 8192;     // bytes of output a warp gathers before it stores
+constexpr uint32_t kPStaging = 2 * 4096; // two rounds of output a warp gathers and stores
 constexpr uint32_t kPSmem = kPStages * kPStageBytes + kPWarps * kPStaging + 1024;
+
+// Registers: the block starts with 168 a thread; the four warps that hold no sums hand theirs over.  What is asked for may not exceed what the block started with.
+constexpr int kPRegs = 65536 / kPThreads / 8 * 8, kPRegsLow = 56, kPRegsHigh = 224;
+static_assert(128 * kPRegsLow + 32 * kPWarps * kPRegsHigh <= kPThreads * kPRegs, "register split");
 
 struct PBars {
     uint64_t full[kPStages], empty[kPStages];  // operand ring (full: the leader's counts for both)
@@ -270,34 +289,80 @@ struct PBars {
     Ctl ctl;
 };
 
-// Stores 32 rows (a lane each, rows `row_stride` apart, valid where `rows` says) x 64 bytes * 4 of
-// output through the warp's staging memory, so that a store covers whole lines: each lane
-// writes its row in pieces of 16 bytes, piece c at place c ^ (row % 16), and the warp then
-// reads two rows at a time.
+// A place in a ring of N and the parity of its current use.
+template <int N>
+struct Turn {
+    int at = 0;
+    uint32_t phase = 0;
+    __device__ __forceinline__ void next() {
+        if (++at == N) at = 0, phase ^= 1u;
+    }
+};
+
+// Stores a warp's 32 tokens (a lane each) x 128 outputs from registers.  The output goes through
+// the warp's two pieces of 4 KB of shared memory in rounds, and from there by TMA (whole lines,
+// tails cut off by the tensor's bounds, and the warp goes on while the copies run); outputs that TMA cannot describe, and channel-major pieces that span two sequences, are
+// stored directly.
 template <typename Tout>
-__device__ __forceinline__ void store_rows(uint8_t* stage, Tout* out, int64_t row_stride, int rows, int lane,
-                                           const f2* acc) {
-    constexpr int kPer = 16 / sizeof(Tout);  // outputs per piece; 16 pieces a row
+__device__ __forceinline__ void store_tile(const LParams& p, const CUtensorMap* mo, uint8_t* stage, int64_t t0,
+                                           int64_t n0, int lane, const float (&acc)[kPCols]) {
+    constexpr int kPer = 16 / sizeof(Tout);   // outputs in 16 bytes
+    constexpr int kRound = 128 / sizeof(Tout);  // token-major: outputs of a 128-byte row
+    constexpr int kRoundCm = 4096 / 32 / sizeof(Tout);  // channel-major: outputs of a 4 KB round
+    const int64_t t = t0 + lane;
+    Tout* out = static_cast<Tout*>(p.out);
+    if (p.seqlen == 0) {
+        if (p.out_tma) {
 #pragma unroll
-    for (int c = 0; c < 16; ++c) {
-        alignas(16) Tout v[kPer];
+            for (int r = 0; r < kPCols / kRound; ++r) {
+                uint8_t* st = stage + (r & 1) * 4096;
+                if (lane == 0) tma_store_wait_read<1>();  // the round before the last has left its piece
+                __syncwarp();
 #pragma unroll
-        for (int j = 0; j < kPer / 2; ++j) {
-            float lo, hi;
-            unpack2(acc[c * (kPer / 2) + j], lo, hi);
-            v[2 * j] = io<Tout>::from_f(lo), v[2 * j + 1] = io<Tout>::from_f(hi);
+                for (int c = 0; c < 8; ++c) {  // 128-byte swizzle: piece c of row i at c ^ (i % 8)
+                    alignas(16) Tout v[kPer];
+#pragma unroll
+                    for (int j = 0; j < kPer; ++j) v[j] = io<Tout>::from_f(acc[r * kRound + c * kPer + j]);
+                    *reinterpret_cast<uint4*>(st + lane * 128 + ((c ^ (lane & 7)) * 16)) =
+                        *reinterpret_cast<uint4*>(v);
+                }
+                fence_proxy_async();
+                __syncwarp();
+                if (lane == 0) {
+                    tma_store_2d(mo, st, (int)n0 + r * kRound, (int)t0);
+                    tma_store_commit();
+                }
+            }
+        } else if (t < p.tokens) {
+            Tout* o = out + t * p.n + n0;
+#pragma unroll
+            for (int c = 0; c < kPCols; ++c)
+                if (n0 + c < p.n) o[c] = io<Tout>::from_f(acc[c]);
         }
-        *reinterpret_cast<uint4*>(stage + lane * 256 + ((c ^ (lane & 15)) * 16)) = *reinterpret_cast<uint4*>(v);
+        return;
     }
-    __syncwarp();
-    const int c = lane & 15;
+    const int64_t b = t0 / p.seqlen, l0 = t0 - b * p.seqlen;
+    if (p.out_tma && (l0 + 32 <= p.seqlen || t0 + (p.seqlen - l0) >= p.tokens)) {
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-        const int r = 2 * i + (lane >> 4);
-        const uint4 v = *reinterpret_cast<const uint4*>(stage + r * 256 + ((c ^ (r & 15)) * 16));
-        if (r < rows) *reinterpret_cast<uint4*>(out + (int64_t)r * row_stride + c * kPer) = v;
+        for (int r = 0; r < kPCols / kRoundCm; ++r) {
+            Tout* st = reinterpret_cast<Tout*>(stage + (r & 1) * 4096);
+            if (lane == 0) tma_store_wait_read<1>();
+            __syncwarp();
+#pragma unroll
+            for (int c = 0; c < kRoundCm; ++c) st[c * 32 + lane] = io<Tout>::from_f(acc[r * kRoundCm + c]);
+            fence_proxy_async();
+            __syncwarp();
+            if (lane == 0) {
+                tma_store_3d(mo, st, (int)l0, (int)n0 + r * kRoundCm, (int)b);
+                tma_store_commit();
+            }
+        }
+    } else if (t < p.tokens) {
+        Tout* o = out + out_index<Tout>(p, t, n0);
+#pragma unroll
+        for (int c = 0; c < kPCols; ++c)
+            if (n0 + c < p.n) o[c * p.seqlen] = io<Tout>::from_f(acc[c]);
     }
-    __syncwarp();
 }
 
 // A pair of CTAs per tile.  In each, warp 0 loads (its 128 tokens and its half of the weight
@@ -307,7 +372,7 @@ __device__ __forceinline__ void store_rows(uint8_t* stage, Tout* out, int64_t ro
 template <typename Tout>
 __global__ void __launch_bounds__(kPThreads, 1)
 prefill_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUtensorMap mw,
-               const LParams p) {
+               const __grid_constant__ CUtensorMap mo, const LParams p) {
     extern __shared__ uint8_t dyn[];
     __shared__ PBars bars;
     uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(dyn) + 1023) & ~(uintptr_t)1023);
@@ -330,51 +395,52 @@ prefill_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ C
     const uint32_t tmem = bars.tmem;
 
     if (warp < 4) {
-        set_registers_down<56>();
+        set_registers_down<kPRegsLow>();
         if (warp == 0) {
             if (elect_one()) {
-                int64_t it = 0;
+                Turn<kPStages> s;
+                int used = 0;  // stages that have been filled
                 bool ok = true;
                 for (int tile = pair; tile < tiles && ok; tile += pairs) {
                     const int tt = tile / p.tiles_n, tn = tile - tt * p.tiles_n;
-                    for (int k = 0; k < p.kb; ++k, ++it) {
-                        const int s = (int)(it % kPStages);
-                        if (!wait_or_abort(&bars.empty[s], (uint32_t)((it / kPStages) & 1) ^ 1u, &bars.ctl)) {
+                    for (int k = 0; k < p.kb; ++k, s.next()) {
+                        if (!wait_or_abort(&bars.empty[s.at], s.phase ^ 1u, &bars.ctl)) {
                             ok = false;
                             break;
                         }
-                        uint8_t* st = ring + s * kPStageBytes;
-                        const uint32_t full = peer_addr(&bars.full[s], 0);
-                        if (rank == 0) mbar_arrive_expect_tx(&bars.full[s], 2 * kPStageBytes);
+                        uint8_t* st = ring + s.at * kPStageBytes;
+                        const uint32_t full = peer_addr(&bars.full[s.at], 0);
+                        if (rank == 0) mbar_arrive_expect_tx(&bars.full[s.at], 2 * kPStageBytes);
                         tma_load_2d_pair(st, &mx, k * kBK, tt * kPT + (int)rank * kBM, full);
                         tma_load_2d_pair(st + kBM * kBK, &mw, k * kBK, tn * kPN + (int)rank * kBM, full);
+                        used = max(used, s.at + 1);
                     }
                 }
                 if (!ok && rank == 0)  // copies in flight (the last use of each stage) before the end
-                    for (int64_t j = it > kPStages ? it - kPStages : 0; j < it; ++j)
-                        mbar_wait_bounded(&bars.full[j % kPStages], (uint32_t)((j / kPStages) & 1), kLimit / 8);
+                    for (int j = 0; j < used; ++j)
+                        mbar_wait_bounded(&bars.full[j], j < s.at ? s.phase : s.phase ^ 1u, kLimit / 8);
             }
         } else if (warp == 1 && rank == 0) {
             if (elect_one()) {
                 constexpr uint32_t idesc = mma_desc(kPT, kPN);
-                int64_t it = 0;
+                Turn<kPStages> s;
+                Turn<2> d;
                 bool ok = true;
                 for (int tile = pair; tile < tiles && ok; tile += pairs) {
-                    for (int k = 0; k < p.kb; ++k, ++it) {
-                        const int s = (int)(it % kPStages), d = (int)(it & 1);
-                        if (!wait_or_abort(&bars.free[d], (uint32_t)((it >> 1) & 1) ^ 1u, &bars.ctl) ||
-                            !wait_or_abort(&bars.full[s], (uint32_t)((it / kPStages) & 1), &bars.ctl)) {
+                    for (int k = 0; k < p.kb; ++k, s.next(), d.next()) {
+                        if (!wait_or_abort(&bars.full[s.at], s.phase, &bars.ctl) ||
+                            !wait_or_abort(&bars.free[d.at], d.phase ^ 1u, &bars.ctl)) {
                             ok = false;
                             break;
                         }
                         tc_fence_after();
-                        const uint32_t a = smem_addr(ring + s * kPStageBytes);
+                        const uint32_t a = smem_addr(ring + s.at * kPStageBytes);
                         const uint64_t da = tile_desc(a), db = tile_desc(a + kBM * kBK);
 #pragma unroll
                         for (int i = 0; i < kBK / 32; ++i)
-                            mma_f8_pair(tmem + d * kPN, da + i * 2, db + i * 2, idesc, i > 0);
-                        tc_commit_pair(&bars.empty[s]);
-                        tc_commit_pair(&bars.done[d]);
+                            mma_f8_pair(tmem + d.at * kPN, da + i * 2, db + i * 2, idesc, i > 0);
+                        tc_commit_pair(&bars.done[d.at]);
+                        tc_commit_pair(&bars.empty[s.at]);
                     }
                 }
                 if (!ok) {
@@ -384,82 +450,60 @@ prefill_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ C
             }
         }
     } else {
-        set_registers_up<224>();
-        const int half = (warp - 4) >> 2, quad = warp & 3;
-        const uint32_t base = tmem + ((uint32_t)(quad * 32) << 16) + half * 128;
+        set_registers_up<kPRegsHigh>();
+        const int part = (warp - 4) >> 2, quad = warp & 3;
+        const uint32_t base = tmem + ((uint32_t)(quad * 32) << 16) + part * kPCols;
         uint8_t* stage = ring + kPStages * kPStageBytes + (warp - 4) * kPStaging;
         const uint32_t free0 = peer_addr(&bars.free[0], 0), free1 = peer_addr(&bars.free[1], 0);
-        int64_t it = 0;
-        bool ok = true;
+        Turn<2> d;
+        uint32_t ra[32], rb[32];
+        bool ok = __all_sync(kFull, wait_or_abort(&bars.done[0], 0, &bars.ctl));
+        tc_fence_after();
+        if (ok) tmem_ld32(base, ra);
         for (int tile = pair; tile < tiles && ok; tile += pairs) {
             const int tt = tile / p.tiles_n, tn = tile - tt * p.tiles_n;
             const int64_t t0 = (int64_t)tt * kPT + rank * kBM + quad * 32;  // the warp's first token
-            const int64_t t = t0 + lane, n0 = (int64_t)tn * kPN + half * 128;
-            const bool in = t < p.tokens && n0 < p.n;
-            const float* xs = p.xs + (in ? t : 0) * p.kb;
+            const int64_t n0 = (int64_t)tn * kPN + part * kPCols;
+            const bool in = t0 + lane < p.tokens && n0 < p.n;
+            const float* xs = p.xs + (in ? t0 + lane : 0) * p.kb;
             const float* ws = p.ws + (in ? n0 / kGroup : 0) * p.kb;
-            f2 acc[64];
+            float acc[kPCols];
 #pragma unroll
-            for (int i = 0; i < 64; ++i) acc[i] = pack2(0.f, 0.f);
+            for (int i = 0; i < kPCols; ++i) acc[i] = 0.f;
             float xn = __ldg(xs), wn = __ldg(ws);
-            for (int k = 0; k < p.kb; ++k, ++it) {
-                const int d = (int)(it & 1);
+            for (int k = 0; k < p.kb; ++k) {
                 const float sc = xn * wn;
                 if (k + 1 < p.kb) xn = __ldg(xs + k + 1), wn = __ldg(ws + k + 1);  // used a block later
-                ok = __all_sync(kFull, wait_or_abort(&bars.done[d], (uint32_t)((it >> 1) & 1), &bars.ctl));
-                if (!ok) break;
-                tc_fence_after();
-                const f2 s2 = pack2(sc, sc);
-#pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                    uint32_t r0[32], r1[32];
-                    tmem_ld32(base + d * kPN + c * 64, r0);
-                    tmem_ld32(base + d * kPN + c * 64 + 32, r1);
-                    tmem_ld_wait(r0, r1);
-                    if (c == 1) {  // the accumulator is in registers: the next products may overwrite it
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) arrive_at(d ? free1 : free0);
-                    }
-#pragma unroll
-                    for (int j = 0; j < 16; ++j) {
-                        acc[c * 32 + j] = fma2(pack2(__uint_as_float(r0[2 * j]), __uint_as_float(r0[2 * j + 1])), s2,
-                                               acc[c * 32 + j]);
-                        acc[c * 32 + 16 + j] = fma2(
-                            pack2(__uint_as_float(r1[2 * j]), __uint_as_float(r1[2 * j + 1])), s2, acc[c * 32 + 16 + j]);
-                    }
+                // Columns in four pieces of 32: the next piece is on its way while one is added.
+                const uint32_t at = base + d.at * kPN;
+                tmem_ld_wait(ra);
+                tmem_ld32(at + 32, rb);
+                add_scaled(acc, ra, sc);
+                tmem_ld_wait(rb);
+                tmem_ld32(at + 64, ra);
+                add_scaled(acc + 32, rb, sc);
+                tmem_ld_wait(ra);
+                tmem_ld32(at + 96, rb);
+                add_scaled(acc + 64, ra, sc);
+                tmem_ld_wait(rb);
+                // the accumulator is in registers: the next products may overwrite it
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) arrive_at(d.at ? free1 : free0);
+                // the first piece of the next block (this tile's or the next one's)
+                d.next();
+                if (k + 1 < p.kb || tile + pairs < tiles) {
+                    ok = __all_sync(kFull, wait_or_abort(&bars.done[d.at], d.phase, &bars.ctl));
+                    if (!ok) break;
+                    tc_fence_after();
+                    tmem_ld32(base + d.at * kPN, ra);
                 }
+                add_scaled(acc + 96, rb, sc);
             }
             if (!ok) break;
-            Tout* out = static_cast<Tout*>(p.out);
-            const int rows = (int)max((int64_t)0, min((int64_t)32, p.tokens - t0));
-            if (n0 >= p.n || rows == 0) continue;
-            if (p.seqlen == 0) {
-                if (n0 + 128 <= p.n && p.n % 8 == 0) {
-                    Tout* o = out + t0 * p.n + n0;
-                    store_rows<Tout>(stage, o, p.n, rows, lane, acc);
-                    if (sizeof(Tout) == 4) store_rows<Tout>(stage, o + 64, p.n, rows, lane, acc + 32);
-                } else if (lane < rows) {
-                    Tout* o = out + t * p.n + n0;
-#pragma unroll
-                    for (int c = 0; c < 64; ++c) {
-                        float v0, v1;
-                        unpack2(acc[c], v0, v1);
-                        if (n0 + 2 * c < p.n) o[2 * c] = io<Tout>::from_f(v0);
-                        if (n0 + 2 * c + 1 < p.n) o[2 * c + 1] = io<Tout>::from_f(v1);
-                    }
-                }
-            } else if (lane < rows) {
-                Tout* o = out + out_index<Tout>(p, t, n0);
-#pragma unroll
-                for (int c = 0; c < 64; ++c) {
-                    float v0, v1;
-                    unpack2(acc[c], v0, v1);
-                    if (n0 + 2 * c < p.n) o[2 * c * p.seqlen] = io<Tout>::from_f(v0);
-                    if (n0 + 2 * c + 1 < p.n) o[(2 * c + 1) * p.seqlen] = io<Tout>::from_f(v1);
-                }
-            }
+            if (n0 < p.n && t0 < p.tokens) store_tile<Tout>(p, &mo, stage, t0, n0, lane, acc);
         }
+        if (lane == 0) tma_store_wait_all();
     }
     tc_fence_before();
     __syncthreads();
@@ -659,11 +703,38 @@ int multiprocessors() {
     return sms;
 }
 
+// The output for the prefill kernel's stores: 32 tokens x 128 bytes of outputs in 128-byte
+// swizzle, or channel-major 32 tokens x 4 KB of outputs.  False where TMA cannot describe it.
+template <typename Tout>
+bool encode_out(CUtensorMap* m, const LinearArgs& a) {
+    const EncodeFn enc = encoder();
+    const int64_t inner = a.seqlen ? a.seqlen : a.n;
+    if (!enc || inner * (int64_t)sizeof(Tout) % 16 != 0) return false;
+    const CUtensorMapDataType dt =
+        sizeof(Tout) == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32;
+    cuuint32_t estr[3] = {1, 1, 1};
+    if (!a.seqlen) {
+        cuuint64_t dims[2] = {(cuuint64_t)a.n, (cuuint64_t)a.tokens};
+        cuuint64_t strides[1] = {(cuuint64_t)a.n * sizeof(Tout)};
+        cuuint32_t box[2] = {128 / sizeof(Tout), 32};
+        return enc(m, dt, 2, a.out, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                   CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    }
+    cuuint64_t dims[3] = {(cuuint64_t)a.seqlen, (cuuint64_t)a.n, (cuuint64_t)(a.tokens / a.seqlen)};
+    cuuint64_t strides[2] = {(cuuint64_t)a.seqlen * sizeof(Tout), (cuuint64_t)a.seqlen * a.n * sizeof(Tout)};
+    cuuint32_t box[3] = {32, 4096 / 32 / sizeof(Tout), 1};
+    return enc(m, dt, 3, a.out, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
+               CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 template <typename Tout>
 cudaError_t run_prefill(const LinearArgs& a, LParams p, cudaStream_t s) {
-    CUtensorMap mx, mw;
+    CUtensorMap mx, mw, mo;
+    memset(&mo, 0, sizeof(mo));
     if (!encode_rows(&mx, a.xq, a.k, a.tokens, kBM) || !encode_rows(&mw, a.wq, a.k, a.n, kBM))
         return cudaErrorInvalidValue;
+    p.out_tma = encode_out<Tout>(&mo, a) ? 1 : 0;
     p.tiles_t = (int)((a.tokens + kPT - 1) / kPT);
     p.tiles_n = (int)((a.n + kPN - 1) / kPN);
     cudaError_t e = cudaFuncSetAttribute(prefill_kernel<Tout>, cudaFuncAttributeMaxDynamicSharedMemorySize, kPSmem);
@@ -681,7 +752,7 @@ cudaError_t run_prefill(const LinearArgs& a, LParams p, cudaStream_t s) {
     attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, prefill_kernel<Tout>, mx, mw, p);
+    return cudaLaunchKernelEx(&cfg, prefill_kernel<Tout>, mx, mw, mo, p);
 }
 
 template <int BN, typename Tout>
@@ -732,7 +803,7 @@ cudaError_t run_linear(const LinearArgs& a, cudaStream_t s) {
     p.n = a.n;
     p.seqlen = a.seqlen;
     p.kb = (int)((a.k + kBK - 1) / kBK);
-    p.tiles_t = p.tiles_n = 0;
+    p.tiles_t = p.tiles_n = p.out_tma = 0;
     const int64_t big = ((a.tokens + kPT - 1) / kPT) * ((a.n + kPN - 1) / kPN);
     if (big >= multiprocessors() / 2) return run_prefill<Tout>(a, p, s);
     if (a.tokens <= 16) return run_token<16, Tout>(a, p, s);
