@@ -570,36 +570,79 @@ def selective_scan_fold(h_ends, delta_sums, A, h0=None, return_delta_sum=False):
 # ---- The gated linear recurrence --------------------------------------------------------
 
 
+# The calls below stand in a decode step's critical path, where a call's host time (about 4 us
+# of it the launch) is longer than its kernel's: they check with as few tensor attribute reads as
+# will do, and go through _check only to say what is wrong.
+
+
 def _cuda_device(t, name, where, ndim):
     if not isinstance(t, torch.Tensor) or t.dim() not in ndim:
         raise ValueError("%s must be a tensor of %s dimensions" % (name, " or ".join(map(str, ndim))))
-    if t.device.type != "cuda":
+    if not t.is_cuda:
         raise ValueError("%s runs on CUDA tensors only" % where)
-    return t.device
+    if not t.is_contiguous():
+        raise ValueError("%s must be contiguous" % name)
+    return t.get_device()
+
+
+def _is(t, name, dev, shape, dtype):
+    """t is a contiguous tensor of this shape and dtype on CUDA device dev; its address."""
+    if (isinstance(t, torch.Tensor) and t.get_device() == dev and t.dtype is dtype and t.shape == shape
+            and t.is_contiguous()):
+        return t.data_ptr()
+    _check(t, name, torch.device("cuda", dev), shape, (dtype,))
+    raise TypeError("%s must be a torch.Tensor" % name)
+
+
+def _output(t, name, like, dev, shape, dtype):
+    """The caller's output, checked, or a new one; and its address."""
+    if t is None:
+        t = _new(like, shape, dtype)
+        return t, t.data_ptr()
+    return t, _is(t, name, dev, shape, dtype)
+
+
+def _maybe(t, name, dev, shape, dtype):
+    return None if t is None else _is(t, name, dev, shape, dtype)
+
+
+def _buffer(t, name, dev):
+    """Address and bytes of a caller's buffer (or None)."""
+    if t is None:
+        return None, 0
+    _check(t, name, torch.device("cuda", dev))
+    return t.data_ptr(), t.numel() * t.element_size()
 
 
 def _dtype(dt, what):
-    if dt not in _DTYPES:
+    code = _DTYPES.get(dt)
+    if code is None:
         raise ValueError("unsupported %s dtype %s" % (what, dt))
-    return _DTYPES[dt]
+    return code
 
 
-def _addr(t):
-    return None if t is None else t.data_ptr()
+def _new(like, shape, dtype):
+    """A new contiguous tensor on like's device (torch.empty_like, where it will do, takes half
+    the time of torch.empty)."""
+    if like.shape == shape and like.is_contiguous():
+        return torch.empty_like(like) if like.dtype is dtype else torch.empty_like(like, dtype=dtype)
+    return torch.empty(shape, dtype=dtype, device=like.device)
 
 
-def _bytes(t):
-    return 0 if t is None else t.numel() * t.element_size()
+# The raw handle of a device's current stream: torch.cuda.current_stream builds a Stream object
+# around it (2.2 us against 0.1).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
 def _run(name, dev, *args):
-    """One library call on dev's current stream; raises MambaError for a non-zero status."""
-    fn = getattr(load_library(), name)
-    if dev.index == torch.cuda.current_device():
-        rc = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
+    """One library call on device dev's current stream; raises MambaError for a non-zero status."""
+    fn = getattr(_lib or load_library(), name)
+    if dev == torch.cuda.current_device():
+        rc = fn(*args, _raw_stream(dev))
     else:
         with torch.cuda.device(dev):
-            rc = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
+            rc = fn(*args, _raw_stream(dev))
     if rc != 0:
         raise MambaError(rc, name)
 
@@ -619,11 +662,11 @@ def gated_scan_bwd_workspace_size(batch: int, dim: int, seqlen: int) -> int:
     return int(load_library().mamba_gated_scan_bwd_workspace_size(GatedDims(batch, dim, seqlen)))
 
 
-def _workspace(workspace, need, dev):
-    if need > 0 and workspace is None:
-        return torch.empty(need, dtype=torch.uint8, device=dev)
-    _check(workspace, "workspace", dev)
-    return workspace
+def _workspace(workspace, need, like, dev):
+    """(the tensor, which the caller keeps until the call has returned, its address, its bytes)"""
+    if workspace is None and need > 0:
+        workspace = _new(like, need, torch.uint8)
+    return (workspace, *_buffer(workspace, "workspace", dev))
 
 
 def gated_scan_fwd(x, gate, gate_bias=None, z=None, initial_state=None, given_decay=False,
@@ -636,30 +679,22 @@ def gated_scan_fwd(x, gate, gate_bias=None, z=None, initial_state=None, given_de
     checkpoints: a uint8 CUDA tensor of gated_scan_checkpoints_size(...) bytes to record what
     ``gated_scan_bwd`` starts from."""
     dev = _cuda_device(x, "x", "gated_scan_fwd", (3,))
-    b, d, L = x.shape
-    in_dt = x.dtype
+    b, d, L = shape = x.shape
+    in_dt, f32 = x.dtype, torch.float32
     out_dt = in_dt if out_dtype is None else out_dtype
     in_code, out_code = _dtype(in_dt, "input"), _dtype(out_dt, "output")
-    f32 = (torch.float32,)
-    _check(x, "x", dev)
-    _check(gate, "gate", dev, (b, d, L), (in_dt,))
-    _check(z, "z", dev, (b, d, L), (in_dt,))
-    _check(gate_bias, "gate_bias", dev, (d,), f32)
-    _check(initial_state, "initial_state", dev, (b, d), f32)
-    if y is None:
-        y = torch.empty((b, d, L), dtype=out_dt, device=dev)
-    else:
-        _check(y, "y", dev, (b, d, L), (out_dt,))
-    if last_state is None and return_last_state:
-        last_state = torch.empty((b, d), dtype=torch.float32, device=dev)
-    _check(last_state, "last_state", dev, (b, d), f32)
-    _check(checkpoints, "checkpoints", dev)
+    y, yp = _output(y, "y", x, dev, shape, out_dt)
+    lp = None
+    if last_state is not None or return_last_state:
+        last_state, lp = _output(last_state, "last_state", x, dev, (b, d), f32)
+    ck, ck_bytes = _buffer(checkpoints, "checkpoints", dev)
     dims = GatedDims(b, d, L)
-    workspace = _workspace(workspace, load_library().mamba_gated_scan_workspace_size(dims), dev)
-    _run("mamba_gated_scan_fwd", dev, x.data_ptr(), gate.data_ptr(), _addr(gate_bias), _addr(z),
-         _addr(initial_state), y.data_ptr(), _addr(last_state), _addr(checkpoints),
-         _bytes(checkpoints), dims, in_code, out_code, _addr(workspace), _bytes(workspace),
-         MAMBA_FLAG_GIVEN_DECAY if given_decay else 0)
+    need = (_lib or load_library()).mamba_gated_scan_workspace_size(dims)
+    workspace, ws, ws_bytes = _workspace(workspace, need, x, dev)
+    _run("mamba_gated_scan_fwd", dev, x.data_ptr(), _is(gate, "gate", dev, shape, in_dt),
+         _maybe(gate_bias, "gate_bias", dev, (d,), f32), _maybe(z, "z", dev, shape, in_dt),
+         _maybe(initial_state, "initial_state", dev, (b, d), f32), yp, lp, ck, ck_bytes, dims, in_code, out_code, ws,
+         ws_bytes, MAMBA_FLAG_GIVEN_DECAY if given_decay else 0)
     return (y, last_state) if return_last_state else y
 
 
@@ -671,29 +706,22 @@ def gated_scan_bwd(x, gate, dy, gate_bias=None, z=None, initial_state=None, dlas
     dinitial_state (batch, dim) fp32.  checkpoints: the buffer the forward filled for the same
     inputs; without it the backward makes one more pass over x and gate."""
     dev = _cuda_device(x, "x", "gated_scan_bwd", (3,))
-    b, d, L = x.shape
-    dt = x.dtype
+    b, d, L = shape = x.shape
+    dt, f32 = x.dtype, torch.float32
     code = _dtype(dt, "input")
-    f32 = (torch.float32,)
-    _check(x, "x", dev)
-    for t, name in ((gate, "gate"), (dy, "dy"), (z, "z")):
-        _check(t, name, dev, (b, d, L), (dt,))
-    _check(gate_bias, "gate_bias", dev, (d,), f32)
-    _check(initial_state, "initial_state", dev, (b, d), f32)
-    _check(dlast_state, "dlast_state", dev, (b, d), f32)
-    _check(checkpoints, "checkpoints", dev)
-    g = dict(dx=torch.empty_like(x), dgate=torch.empty_like(x),
-             dz=None if z is None else torch.empty_like(x),
-             dgate_bias=None if gate_bias is None or given_decay
-             else torch.empty(d, dtype=torch.float32, device=dev),
-             dinitial_state=torch.empty((b, d), dtype=torch.float32, device=dev))
+    g = dict(dx=_new(x, shape, dt), dgate=_new(x, shape, dt), dz=None if z is None else _new(x, shape, dt),
+             dgate_bias=None if gate_bias is None or given_decay else _new(x, (d,), f32),
+             dinitial_state=_new(x, (b, d), f32))
+    ck, ck_bytes = _buffer(checkpoints, "checkpoints", dev)
     dims = GatedDims(b, d, L)
-    workspace = _workspace(workspace, load_library().mamba_gated_scan_bwd_workspace_size(dims), dev)
-    _run("mamba_gated_scan_bwd", dev, x.data_ptr(), gate.data_ptr(), _addr(gate_bias), _addr(z),
-         _addr(initial_state), dy.data_ptr(), _addr(dlast_state), g["dx"].data_ptr(),
-         g["dgate"].data_ptr(), _addr(g["dz"]), _addr(g["dgate_bias"]),
-         g["dinitial_state"].data_ptr(), _addr(checkpoints), _bytes(checkpoints), dims, code,
-         _addr(workspace), _bytes(workspace), MAMBA_FLAG_GIVEN_DECAY if given_decay else 0)
+    need = (_lib or load_library()).mamba_gated_scan_bwd_workspace_size(dims)
+    workspace, ws, ws_bytes = _workspace(workspace, need, x, dev)
+    _run("mamba_gated_scan_bwd", dev, x.data_ptr(), _is(gate, "gate", dev, shape, dt),
+         _maybe(gate_bias, "gate_bias", dev, (d,), f32), _maybe(z, "z", dev, shape, dt),
+         _maybe(initial_state, "initial_state", dev, (b, d), f32), _is(dy, "dy", dev, shape, dt),
+         _maybe(dlast_state, "dlast_state", dev, (b, d), f32), g["dx"].data_ptr(), g["dgate"].data_ptr(),
+         _addr(g["dz"]), _addr(g["dgate_bias"]), g["dinitial_state"].data_ptr(), ck, ck_bytes, dims,
+         code, ws, ws_bytes, MAMBA_FLAG_GIVEN_DECAY if given_decay else 0)
     return g
 
 
@@ -702,42 +730,47 @@ def gated_state_update(state, x, gate, gate_bias=None, z=None, given_decay=False
     x, gate, z: (batch, dim).  Returns y (batch, dim)."""
     dev = _cuda_device(state, "state", "gated_state_update", (2,))
     b, d = shape = state.shape
+    f32 = torch.float32
+    if not isinstance(x, torch.Tensor):
+        raise TypeError("x must be a torch.Tensor")
     dt = x.dtype
     code = _dtype(dt, "input")
-    _check(state, "state", dev, shape, (torch.float32,))
-    _check(x, "x", dev, shape)
-    _check(gate, "gate", dev, shape, (dt,))
-    _check(z, "z", dev, shape, (dt,))
-    _check(gate_bias, "gate_bias", dev, (d,), (torch.float32,))
-    if y is None:
-        y = torch.empty_like(x)
-    else:
-        _check(y, "y", dev, shape, (dt,))
-    _run("mamba_gated_state_update", dev, state.data_ptr(), x.data_ptr(), gate.data_ptr(),
-         _addr(gate_bias), _addr(z), y.data_ptr(), b, d, code,
+    xp = _is(x, "x", dev, shape, dt)
+    y, yp = _output(y, "y", x, dev, shape, dt)
+    _run("mamba_gated_state_update", dev, _is(state, "state", dev, shape, f32), xp, _is(gate, "gate", dev, shape, dt), _maybe(gate_bias, "gate_bias", dev, (d,), f32),
+         _maybe(z, "z", dev, shape, dt), yp, b, d, code,
          MAMBA_FLAG_GIVEN_DECAY if given_decay else 0)
     return y
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
 
 
 # ---- Residual addition with RMS norm ----------------------------------------------------
 
 
 def _norm_inputs(x, weight, residual, residual_out, where):
+    """(device, dim, rows, dtype codes, the addresses of x, residual, weight, residual_out, and
+    residual_out itself)"""
     dev = _cuda_device(x, "x", where, (2, 3))
-    d = x.shape[-1]
-    code = _dtype(x.dtype, "input")
-    _check(x, "x", dev)
-    _check(weight, "weight", dev, (d,), (torch.float32,))
-    rt = x.dtype
+    shape, dt = x.shape, x.dtype
+    d = shape[-1]
+    code = rcode = _dtype(dt, "input")
+    rt, rp = dt, None
     if residual is not None:
-        _check(residual, "residual", dev, x.shape)
+        if not isinstance(residual, torch.Tensor):
+            raise TypeError("residual must be a torch.Tensor")
         rt = residual.dtype
-    rcode = _dtype(rt, "residual")
-    if residual_out is None:
-        residual_out = torch.empty_like(residual) if residual is not None else None
-    else:
-        _check(residual_out, "residual_out", dev, x.shape, (rt,))
-    return dev, d, code, rcode, residual_out
+        rcode = _dtype(rt, "residual")
+        rp = _is(residual, "residual", dev, shape, rt)
+    op = None
+    if residual is not None or residual_out is not None:
+        residual_out, op = _output(residual_out, "residual_out", x if residual is None else residual, dev,
+                                   shape, rt)
+    rows = shape[0] if len(shape) == 2 else shape[0] * shape[1]
+    return (dev, d, rows, code, rcode, x.data_ptr(), rp,
+            _is(weight, "weight", dev, (d,), torch.float32), op, residual_out)
 
 
 def add_rms_norm_fwd(x, weight, residual=None, eps=1e-5, out_dtype=None, out=None,
@@ -745,43 +778,31 @@ def add_rms_norm_fwd(x, weight, residual=None, eps=1e-5, out_dtype=None, out=Non
     """v = residual + x (in the residual's dtype); out = v / sqrt(mean v^2 + eps) * weight.
     x, residual: (..., dim) of 2 or 3 dimensions, weight: (dim) fp32.  Returns (out, v);
     without a residual v is x."""
-    dev, d, code, rcode, residual_out = _norm_inputs(x, weight, residual, residual_out,
-                                                     "add_rms_norm_fwd")
+    dev, d, rows, code, rcode, xp, rp, wp, op, residual_out = _norm_inputs(
+        x, weight, residual, residual_out, "add_rms_norm_fwd")
     out_dt = x.dtype if out_dtype is None else out_dtype
     ocode = _dtype(out_dt, "output")
-    if out is None:
-        out = torch.empty(x.shape, dtype=out_dt, device=dev)
-    else:
-        _check(out, "out", dev, x.shape, (out_dt,))
-    _run("mamba_add_rms_norm_fwd", dev, x.data_ptr(), _addr(residual), weight.data_ptr(), eps,
-         out.data_ptr(), _addr(residual_out), x.numel() // d if d else 0, d, code, rcode, ocode)
+    out, outp = _output(out, "out", x, dev, x.shape, out_dt)
+    _run("mamba_add_rms_norm_fwd", dev, xp, rp, wp, eps, outp, op, rows, d, code, rcode, ocode)
     return out, x if residual_out is None else residual_out
 
 
 def add_rms_norm_fp8(x, weight, residual=None, eps=1e-5, q=None, scales=None, residual_out=None):
     """``add_rms_norm_fwd`` with the output in e4m3: returns (q (..., dim) float8_e4m3fn,
     scales (..., ceil(dim / 128)) fp32, v), out = q * scale.  dim a multiple of 16."""
-    dev, d, code, rcode, residual_out = _norm_inputs(x, weight, residual, residual_out,
-                                                     "add_rms_norm_fp8")
-    lead = tuple(x.shape[:-1])
-    q, scales = _fp8_outputs(q, scales, lead, d, dev)
-    _run("mamba_add_rms_norm_fp8", dev, x.data_ptr(), _addr(residual), weight.data_ptr(), eps,
-         q.data_ptr(), scales.data_ptr(), _addr(residual_out), x.numel() // d if d else 0, d, code,
-         rcode)
+    dev, d, rows, code, rcode, xp, rp, wp, op, residual_out = _norm_inputs(
+        x, weight, residual, residual_out, "add_rms_norm_fp8")
+    q, scales, qp, sp = _fp8_outputs(x, q, scales, x.shape[:-1], d, dev)
+    _run("mamba_add_rms_norm_fp8", dev, xp, rp, wp, eps, qp, sp, op, rows, d, code, rcode)
     return q, scales, x if residual_out is None else residual_out
 
 
-def _fp8_outputs(q, scales, lead, d, dev):
-    if q is None:
-        q = torch.empty(lead + (d,), dtype=torch.float8_e4m3fn, device=dev)
-    else:
-        _check(q, "q", dev, lead + (d,), (torch.float8_e4m3fn,))
-    groups = (d + 127) // 128
-    if scales is None:
-        scales = torch.empty(lead + (groups,), dtype=torch.float32, device=dev)
-    else:
-        _check(scales, "scales", dev, lead + (groups,), (torch.float32,))
-    return q, scales
+def _fp8_outputs(like, q, scales, lead, d, dev):
+    """e4m3 rows and their scales (new ones where None), and their addresses."""
+    qs, ss = (*lead, d), (*lead, (d + 127) // 128)
+    q, qp = _output(q, "q", like, dev, qs, torch.float8_e4m3fn)
+    scales, sp = _output(scales, "scales", like, dev, ss, torch.float32)
+    return q, scales, qp, sp
 
 
 def add_rms_norm_bwd(dout, residual_out, weight, dresidual_out=None, eps=1e-5, workspace=None):
@@ -790,23 +811,22 @@ def add_rms_norm_bwd(dout, residual_out, weight, dresidual_out=None, eps=1e-5, w
     dict: dx (dout's dtype), dresidual (v's dtype; the same tensor where the dtypes agree),
     dweight (dim) fp32."""
     dev = _cuda_device(dout, "dout", "add_rms_norm_bwd", (2, 3))
-    d = dout.shape[-1]
-    code = _dtype(dout.dtype, "input")
-    _check(dout, "dout", dev)
-    _check(residual_out, "residual_out", dev, dout.shape)
+    shape, dt, f32 = dout.shape, dout.dtype, torch.float32
+    d = shape[-1]
+    code = _dtype(dt, "input")
+    if not isinstance(residual_out, torch.Tensor):
+        raise TypeError("residual_out must be a torch.Tensor")
     rt = residual_out.dtype
     rcode = _dtype(rt, "residual")
-    _check(weight, "weight", dev, (d,), (torch.float32,))
-    _check(dresidual_out, "dresidual_out", dev, dout.shape, (rt,))
-    dx = torch.empty_like(dout)
-    dres = None if rt == dout.dtype else torch.empty_like(residual_out)
-    dw = torch.empty(d, dtype=torch.float32, device=dev)
-    rows = dout.numel() // d if d else 0
-    workspace = _workspace(workspace, load_library().mamba_add_rms_norm_bwd_workspace_size(rows, d),
-                           dev)
-    _run("mamba_add_rms_norm_bwd", dev, dout.data_ptr(), residual_out.data_ptr(), weight.data_ptr(),
-         _addr(dresidual_out), eps, dx.data_ptr(), _addr(dres), dw.data_ptr(), rows, d, code, rcode,
-         _addr(workspace), _bytes(workspace))
+    dx = _new(dout, shape, dt)
+    dres = None if rt == dt else _new(dout, shape, rt)
+    dw = _new(dout, (d,), f32)
+    rows = shape[0] if len(shape) == 2 else shape[0] * shape[1]
+    need = (_lib or load_library()).mamba_add_rms_norm_bwd_workspace_size(rows, d)
+    workspace, ws, ws_bytes = _workspace(workspace, need, dout, dev)
+    _run("mamba_add_rms_norm_bwd", dev, dout.data_ptr(), _is(residual_out, "residual_out", dev, shape, rt), _is(weight, "weight", dev, (d,), f32),
+         _maybe(dresidual_out, "dresidual_out", dev, shape, rt), eps, dx.data_ptr(), _addr(dres),
+         dw.data_ptr(), rows, d, code, rcode, ws, ws_bytes)
     return dict(dx=dx, dresidual=dx if dres is None else dres, dweight=dw)
 
 
@@ -820,11 +840,10 @@ def fp8_quantize(x, channel_major=False, q=None, scales=None):
     case.  dim a multiple of 16."""
     dev = _cuda_device(x, "x", "fp8_quantize", (3,) if channel_major else (2,))
     code = _dtype(x.dtype, "input")
-    _check(x, "x", dev)
     b, d, L = x.shape if channel_major else (1, x.shape[1], x.shape[0])
-    q, scales = _fp8_outputs(q, scales, (b * L,), d, dev)
-    _run("mamba_fp8_quantize", dev, x.data_ptr(), q.data_ptr(), scales.data_ptr(), b, d, L,
-         int(bool(channel_major)), code)
+    q, scales, qp, sp = _fp8_outputs(x, q, scales, (b * L,), d, dev)
+    _run("mamba_fp8_quantize", dev, x.data_ptr(), qp, sp, b, d, L,
+         1 if channel_major else 0, code)
     return q, scales
 
 
@@ -833,11 +852,11 @@ def fp8_quantize_weight(w):
     float8_e4m3fn, scales (ceil(n / 128), ceil(k / 128)) fp32).  k a multiple of 16."""
     dev = _cuda_device(w, "w", "fp8_quantize_weight", (2,))
     code = _dtype(w.dtype, "input")
-    _check(w, "w", dev)
     n, k = w.shape
-    q = torch.empty((n, k), dtype=torch.float8_e4m3fn, device=dev)
-    scales = torch.empty(((n + 127) // 128, (k + 127) // 128), dtype=torch.float32, device=dev)
-    _run("mamba_fp8_quantize_weight", dev, w.data_ptr(), q.data_ptr(), scales.data_ptr(), n, k, code)
+    q = _new(w, (n, k), torch.float8_e4m3fn)
+    scales = _new(w, ((n + 127) // 128, (k + 127) // 128), torch.float32)
+    _run("mamba_fp8_quantize_weight", dev, w.data_ptr(), q.data_ptr(),
+         scales.data_ptr(), n, k, code)
     return q, scales
 
 
@@ -850,21 +869,15 @@ def fp8_linear(xq, x_scales, wq, w_scales, out_dtype=torch.bfloat16, channel_maj
     code = _dtype(out_dtype, "output")
     t, k = xq.shape
     n = wq.shape[0] if isinstance(wq, torch.Tensor) and wq.dim() == 2 else -1
-    f8, f32, kb = (torch.float8_e4m3fn,), (torch.float32,), (k + 127) // 128
-    _check(xq, "xq", dev, None, f8)
-    _check(x_scales, "x_scales", dev, (t, kb), f32)
-    _check(wq, "wq", dev, (n, k), f8)
-    _check(w_scales, "w_scales", dev, ((n + 127) // 128, kb), f32)
-    L = 0
+    f8, f32, kb = torch.float8_e4m3fn, torch.float32, (k + 127) // 128
+    L, shape = 0, (t, n)
     if channel_major_seqlen is not None:
         L = int(channel_major_seqlen)
         if L < 1 or t % L != 0:
             raise ValueError("channel_major_seqlen must be positive and divide the %d tokens" % t)
-    shape = (t, n) if L == 0 else (t // L, n, L)
-    if out is None:
-        out = torch.empty(shape, dtype=out_dtype, device=dev)
-    else:
-        _check(out, "out", dev, shape, (out_dtype,))
-    _run("mamba_fp8_linear", dev, xq.data_ptr(), x_scales.data_ptr(), wq.data_ptr(),
-         w_scales.data_ptr(), out.data_ptr(), t, n, k, L, code)
+        shape = (t // L, n, L)
+    ptrs = (_is(xq, "xq", dev, (t, k), f8), _is(x_scales, "x_scales", dev, (t, kb), f32),
+            _is(wq, "wq", dev, (n, k), f8), _is(w_scales, "w_scales", dev, ((n + 127) // 128, kb), f32))
+    out, outp = _output(out, "out", xq, dev, shape, out_dtype)
+    _run("mamba_fp8_linear", dev, *ptrs, outp, t, n, k, L, code)
     return out
