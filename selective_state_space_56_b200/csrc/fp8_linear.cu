@@ -15,7 +15,7 @@
 //                    weights' share of the shared-memory traffic that a 128 x 256 tile of one CTA is
 //                    bound by.  A lane is a token, so its scale is one register a block.
 //   token_kernel     few tokens: bound by the weights' bytes.  128 outputs are the MMA's rows,
-//                    the tokens its columns (16 to 128), and the inputs are cut into pieces over a
+//                    the tokens its columns (16 to 64), and the inputs are cut into pieces over a
 //                    cluster whose CTAs add their sums through distributed shared memory in
 //                    a fixed order.
 //
@@ -25,6 +25,7 @@
 #include <cudaTypedefs.h>
 
 #include <algorithm>
+#include <atomic>
 #include <cstring>
 #include <mutex>
 
@@ -515,10 +516,12 @@ prefill_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ C
 // ---- Few tokens ------------------------------------------------------------------------
 
 constexpr int kTThreads = 192;  // warps 0-3 keep the sums, warp 4 loads, warp 5 issues products
+constexpr int kTStages = 6;     // at most, of the operand ring
+constexpr int kTTurns = 8;      // at most, accumulators in tensor memory
 
 struct TBars {
-    uint64_t full[6], empty[6];
-    uint64_t done[2], free[2];
+    uint64_t full[kTStages], empty[kTStages];
+    uint64_t done[kTTurns], free[kTTurns];
     uint64_t drain;
     uint32_t tmem;
     Ctl ctl;
@@ -526,16 +529,23 @@ struct TBars {
 
 template <int BN>
 constexpr uint32_t token_stage_bytes() { return (kBM + BN) * kBK; }
+// Accumulators kept at once: as many as fit in half of tensor memory (two CTAs share an SM).
+template <int BN>
+constexpr int token_turns() { return 256 / BN < kTTurns ? 256 / BN : kTTurns; }
+constexpr int kTPitch = kBM + 4;  // floats between the sums of two tokens
 
-__device__ __forceinline__ float peer_load(const float* local, uint32_t rank) {
-    float v;
-    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(peer_addr(local, rank)) : "memory");
+__device__ __forceinline__ float4 peer_load4(uint32_t cluster_addr) {
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "r"(cluster_addr)
+                 : "memory");
     return v;
 }
 
 // Grid (pieces, output tiles, token tiles), a cluster of `pieces` CTAs along x.  Piece q takes
 // input blocks [kb q / pieces, kb (q + 1) / pieces); the pieces' sums are added in order of
-// piece, each CTA adding and storing its share of the tile's columns.
+// piece, each CTA adding and storing its share of the tile's outputs.
 template <int BN, typename Tout>
 __global__ void __launch_bounds__(kTThreads)
 token_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUtensorMap mw,
@@ -544,82 +554,86 @@ token_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUt
     __shared__ TBars bars;
     uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(dyn) + 1023) & ~(uintptr_t)1023);
     constexpr uint32_t kStage = token_stage_bytes<BN>();
-    constexpr uint32_t kCols = 2 * BN < 32 ? 32 : 2 * BN;
-    float* red = reinterpret_cast<float*>(ring);                        // [BN][128], after the products
+    constexpr int kTurns = token_turns<BN>();
+    constexpr uint32_t kCols = kTurns * BN;
+    float* red = reinterpret_cast<float*>(ring);                        // [BN][kTPitch], after the products
     float* scl = reinterpret_cast<float*>(ring + (size_t)stages * kStage);  // [blocks][BN] scales
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int pieces = (int)gridDim.x, piece = (int)cluster_rank();
     const int k0 = (int)((int64_t)p.kb * piece / pieces), k1 = (int)((int64_t)p.kb * (piece + 1) / pieces);
     const int64_t n0 = (int64_t)blockIdx.y * kBM, t0 = (int64_t)blockIdx.z * BN;
-    if (threadIdx.x == 0) {
+    if (threadIdx.x == 128) {
         for (int i = 0; i < stages; ++i) mbar_init(&bars.full[i], 1), mbar_init(&bars.empty[i], 1);
-        for (int i = 0; i < 2; ++i) mbar_init(&bars.done[i], 1), mbar_init(&bars.free[i], 4);
+        for (int i = 0; i < kTurns; ++i) mbar_init(&bars.done[i], 1), mbar_init(&bars.free[i], 4);
         mbar_init(&bars.drain, 1);
         bars.ctl.abort = 0;
         fence_barrier_init();
     }
     if (warp == 5) tmem_alloc(&bars.tmem, kCols);
-    // token scales times the tile's weight scales, by block and column
-    if (warp < 4)
-        for (int i = threadIdx.x; i < (k1 - k0) * BN; i += 128) {
-            const int c = i % BN, k = i / BN;
-            const int64_t t = t0 + c;
-            scl[i] = t < p.tokens ? __ldg(p.xs + t * p.kb + k0 + k) * __ldg(p.ws + (n0 / kGroup) * p.kb + k0 + k)
-                                  : 0.f;
-        }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = bars.tmem;
-    bool ok = true;
     if (warp == 4) {
         if (elect_one()) {
+            int s = 0;
+            uint32_t phase = 0;
             for (int k = k0; k < k1; ++k) {
-                const int it = k - k0, s = it % stages;
-                if (!wait_or_abort(&bars.empty[s], (uint32_t)((it / stages) & 1) ^ 1u, &bars.ctl)) {
-                    for (int j = it > stages ? it - stages : 0; j < it; ++j)
-                        mbar_wait_bounded(&bars.full[j % stages], (uint32_t)((j / stages) & 1), kLimit / 8);
+                if (!wait_or_abort(&bars.empty[s], phase ^ 1u, &bars.ctl)) {
+                    for (int j = 0; j < min(stages, k - k0); ++j)  // copies in flight
+                        mbar_wait_bounded(&bars.full[j], j < s ? phase : phase ^ 1u, kLimit / 8);
                     break;
                 }
                 uint8_t* st = ring + (size_t)s * kStage;
                 mbar_arrive_expect_tx(&bars.full[s], kStage);
                 tma_load_2d(st, &mw, k * kBK, (int)n0, &bars.full[s]);
                 tma_load_2d(st + kBM * kBK, &mx, k * kBK, (int)t0, &bars.full[s]);
+                if (++s == stages) s = 0, phase ^= 1u;
             }
         }
     } else if (warp == 5) {
         if (elect_one()) {
             constexpr uint32_t idesc = mma_desc(kBM, BN);
-            for (int k = k0; k < k1; ++k) {
-                const int it = k - k0, s = it % stages, d = it & 1;
-                if (!wait_or_abort(&bars.free[d], (uint32_t)((it >> 1) & 1) ^ 1u, &bars.ctl) ||
-                    !wait_or_abort(&bars.full[s], (uint32_t)((it / stages) & 1), &bars.ctl)) {
+            int s = 0;
+            uint32_t phase = 0;
+            Turn<kTurns> d;
+            for (int k = k0; k < k1; ++k, d.next()) {
+                if (!wait_or_abort(&bars.free[d.at], d.phase ^ 1u, &bars.ctl) ||
+                    !wait_or_abort(&bars.full[s], phase, &bars.ctl)) {
                     tc_commit(&bars.drain);
                     mbar_wait_bounded(&bars.drain, 0, kLimit / 8);
                     break;
                 }
                 tc_fence_after();
                 const uint32_t a = smem_addr(ring + (size_t)s * kStage);
-                mma_stage(tmem + d * BN, a, a + kBM * kBK, idesc);
+                mma_stage(tmem + d.at * BN, a, a + kBM * kBK, idesc);
+                tc_commit(&bars.done[d.at]);
                 tc_commit(&bars.empty[s]);
-                tc_commit(&bars.done[d]);
+                if (++s == stages) s = 0, phase ^= 1u;
             }
         }
     } else {
+        // token scales times the tile's weight scales, by block and column, while the tiles load
+        const float* ws = p.ws + (n0 / kGroup) * p.kb + k0;
+#pragma unroll 4
+        for (int i = threadIdx.x; i < (k1 - k0) * BN; i += 128) {
+            const int c = i % BN, k = i / BN;
+            scl[i] = t0 + c < p.tokens ? __ldg(p.xs + (t0 + c) * p.kb + k0 + k) * __ldg(ws + k) : 0.f;
+        }
+        asm volatile("bar.sync 1, 128;" ::: "memory");
         const uint32_t base = tmem + ((uint32_t)(warp * 32) << 16);
         float acc[BN];
 #pragma unroll
         for (int i = 0; i < BN; ++i) acc[i] = 0.f;
-        for (int k = k0; k < k1; ++k) {
-            const int it = k - k0, d = it & 1;
-            ok = __all_sync(kFull, wait_or_abort(&bars.done[d], (uint32_t)((it >> 1) & 1), &bars.ctl));
-            if (!ok) break;
+        Turn<kTurns> d;
+        for (int k = k0; k < k1; ++k, d.next()) {
+            if (!__all_sync(kFull, wait_or_abort(&bars.done[d.at], d.phase, &bars.ctl))) break;
             tc_fence_after();
-            const float* sc = scl + it * BN;
+            const float* sc = scl + (k - k0) * BN;
 #pragma unroll
             for (int c = 0; c < BN / 16; ++c) {
                 uint32_t r[16];
-                tmem_ld16(base + d * BN + c * 16, r);
+                tmem_ld16(base + d.at * BN + c * 16, r);
                 tmem_ld_wait(r);
 #pragma unroll
                 for (int j = 0; j < 16; j += 4) {
@@ -632,14 +646,14 @@ token_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUt
             }
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&bars.free[d]);
+            if (lane == 0) mbar_arrive(&bars.free[d.at]);
         }
         // All of this CTA's products are done (each was waited for), and with them its operand
         // tiles: the ring takes the sums.
         asm volatile("bar.sync 1, 128;" ::: "memory");
         if (!bars.ctl.abort) {
 #pragma unroll
-            for (int i = 0; i < BN; ++i) red[i * kBM + warp * 32 + lane] = acc[i];
+            for (int i = 0; i < BN; ++i) red[i * kTPitch + warp * 32 + lane] = acc[i];
         }
     }
     tc_fence_before();
@@ -650,16 +664,45 @@ token_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUt
     __syncwarp();
     cluster_sync();
     if (!bad) {
-        // this CTA's columns (tokens) of the tile
-        const int c0 = BN * piece / pieces, c1 = BN * (piece + 1) / pieces;
+        // This CTA's share of the 128 outputs of every token, four at a time.  Channel-major, the
+        // lanes run along the tokens, which are the output's inner axis.
+        const int quad0 = kBM / 4 * piece / pieces, quads = kBM / 4 * (piece + 1) / pieces - quad0;
+        const bool along_tokens = p.seqlen > 1;
+        uint32_t peer[8];
+#pragma unroll
+        for (int q = 0; q < 8; ++q) peer[q] = peer_addr(red, (uint32_t)(q < pieces ? q : 0));
         Tout* out = static_cast<Tout*>(p.out);
-        for (int i = threadIdx.x; i < (c1 - c0) * kBM; i += kTThreads) {
-            const int c = c0 + i / kBM, row = i % kBM;
+        const int64_t b0 = along_tokens ? t0 / p.seqlen : 0;
+        for (int i = threadIdx.x; i < quads * BN; i += kTThreads) {
+            const int c = along_tokens ? i % BN : i / quads;
+            const int row = (quad0 + (along_tokens ? i / BN : i % quads)) * 4;
             const int64_t t = t0 + c, n = n0 + row;
             if (t >= p.tokens || n >= p.n) continue;
-            float v = 0.f;
-            for (int q = 0; q < pieces; ++q) v += peer_load(red + c * kBM + row, (uint32_t)q);
-            out[out_index<Tout>(p, t, n)] = io<Tout>::from_f(v);
+            float4 u[8];
+#pragma unroll
+            for (int q = 0; q < 8; ++q)
+                if (q < pieces) u[q] = peer_load4(peer[q] + (uint32_t)(c * kTPitch + row) * 4);
+            float v[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int q = 0; q < 8; ++q)
+                if (q < pieces) v[0] += u[q].x, v[1] += u[q].y, v[2] += u[q].z, v[3] += u[q].w;
+            if (along_tokens) {
+                int64_t b = b0, l = t - b0 * p.seqlen;
+                while (l >= p.seqlen) l -= p.seqlen, ++b;
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    if (n + j < p.n) out[(b * p.n + n + j) * p.seqlen + l] = io<Tout>::from_f(v[j]);
+            } else if (p.n % 4 == 0) {
+                alignas(16) Tout o[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) o[j] = io<Tout>::from_f(v[j]);
+                struct alignas(4 * sizeof(Tout)) Four { Tout o[4]; };
+                *reinterpret_cast<Four*>(out + t * p.n + n) = *reinterpret_cast<const Four*>(o);
+            } else {
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    if (n + j < p.n) out[t * p.n + n + j] = io<Tout>::from_f(v[j]);
+            }
         }
     }
     cluster_sync();  // a CTA's shared memory outlives its peers' reads
@@ -695,11 +738,15 @@ bool encode_rows(CUtensorMap* m, const void* base, int64_t k, int64_t rows, int 
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Multiprocessors of the current device, asked once per device.
 int multiprocessors() {
+    static std::atomic<int> known[64];
     int dev = 0, sms = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess ||
-        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms < 1)
-        return 148;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 148;
+    sms = known[dev].load(std::memory_order_relaxed);
+    if (sms > 0) return sms;
+    if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms < 1) return 148;
+    known[dev].store(sms, std::memory_order_relaxed);
     return sms;
 }
 
@@ -755,22 +802,53 @@ cudaError_t run_prefill(const LinearArgs& a, LParams p, cudaStream_t s) {
     return cudaLaunchKernelEx(&cfg, prefill_kernel<Tout>, mx, mw, mo, p);
 }
 
+// Pieces of the inputs per tile: up to 8 (a portable cluster), while all pieces run at once and
+// each has at least two blocks.  Two CTAs fit on an SM; clusters of three and more do not fill
+// every SM of a GPC, so they get a ninth fewer places.
+int token_pieces(int64_t tiles, int kb) {
+    const int64_t slots = 2 * (int64_t)multiprocessors();
+    int64_t pieces = 8;
+    while (pieces > 1 && (tiles * pieces > (pieces > 2 ? slots * 8 / 9 : slots) || pieces * 2 > kb)) --pieces;
+    return (int)pieces;
+}
+
+// Columns (tokens) of the token kernel's tiles.
+int token_columns(int64_t tokens) { return tokens <= 16 ? 16 : tokens <= 32 ? 32 : 64; }
+
+// Whether the prefill kernel is the faster one.  Both times are close to straight lines in the
+// input blocks walked one after another, fitted to launches of (64 .. 4096 tokens) x (768 .. 10240
+// outputs) x (1536 .. 5120 inputs), weights in L2:
+//   prefill  7 us + 0.43 us a block and wave of 74 tiles of 256 x 256
+//   token    5 us + 0.80 us a block, longer in proportion once the CTAs exceed two an SM
+// (128 tokens, 2560 -> 10240: 16.4 against 19.8 us; 64 tokens: 15.7 against 11.4; 256 tokens,
+// 5120 -> 2560: 25.2 against 15.4; 1024 tokens: 26.8 against 50).
+bool prefill_is_faster(const LinearArgs& a, int kb) {
+    const int64_t sms = multiprocessors();
+    const int64_t big = ((a.tokens + kPT - 1) / kPT) * ((a.n + kPN - 1) / kPN);
+    const int64_t pairs = std::max<int64_t>(1, sms / 2);
+    const double prefill = 7.0 + 0.43 * kb * (double)((big + pairs - 1) / pairs);
+    const int bn = token_columns(a.tokens);
+    const int64_t tiles = ((a.n + kBM - 1) / kBM) * ((a.tokens + bn - 1) / bn);
+    const int pieces = token_pieces(tiles, kb);
+    const double full = 1.1 * (double)(tiles * pieces) / (double)(2 * sms);
+    const double token = 5.0 + 0.8 * ((kb + pieces - 1) / pieces) * std::max(1.0, full);
+    return prefill < token;
+}
+
 template <int BN, typename Tout>
 cudaError_t run_token(const LinearArgs& a, const LParams& p, cudaStream_t s) {
     CUtensorMap mx, mw;
     if (!encode_rows(&mx, a.xq, a.k, a.tokens, BN) || !encode_rows(&mw, a.wq, a.k, a.n, kBM))
         return cudaErrorInvalidValue;
     const int64_t tn = (a.n + kBM - 1) / kBM, tt = (a.tokens + BN - 1) / BN;
-    // pieces: up to 8 (a portable cluster), while they fill the machine's CTA slots twice over and
-    // leave every piece two blocks
-    int pieces = 1;
-    while (pieces < 8 && pieces * 2 <= BN && tn * tt * pieces < multiprocessors() * 2 && pieces * 4 <= p.kb)
-        pieces *= 2;
+    const int pieces = token_pieces(tn * tt, p.kb);
     const int blocks = (p.kb + pieces - 1) / pieces;
     constexpr uint32_t kStage = token_stage_bytes<BN>();
-    constexpr int kLeast = (BN * kBM * 4 + kStage - 1) / kStage;  // the ring also holds the tile's sums
+    constexpr int kLeast = (BN * kTPitch * 4 + kStage - 1) / kStage;  // the ring also holds the tile's sums
+    static_assert(kLeast <= kTStages, "the sums fit in the ring");
     constexpr int64_t kMost = 226 * 1024;
-    int stages = std::max(std::min(blocks, 6), kLeast);
+    // a ring that leaves room for a second CTA on the SM
+    int stages = std::max(std::min<int>(blocks, std::min<int>(kTStages, 100 * 1024 / kStage)), kLeast);
     const int64_t scales = (int64_t)blocks * BN * 4 + 1024;
     while (stages > kLeast && stages * (int64_t)kStage + scales > kMost) --stages;
     if (stages * (int64_t)kStage + scales > kMost) return run_prefill<Tout>(a, p, s);  // k above 80,000
@@ -804,11 +882,12 @@ cudaError_t run_linear(const LinearArgs& a, cudaStream_t s) {
     p.seqlen = a.seqlen;
     p.kb = (int)((a.k + kBK - 1) / kBK);
     p.tiles_t = p.tiles_n = p.out_tma = 0;
-    const int64_t big = ((a.tokens + kPT - 1) / kPT) * ((a.n + kPN - 1) / kPN);
-    if (big >= multiprocessors() / 2) return run_prefill<Tout>(a, p, s);
-    if (a.tokens <= 16) return run_token<16, Tout>(a, p, s);
-    if (a.tokens <= 32) return run_token<32, Tout>(a, p, s);
-    return run_token<64, Tout>(a, p, s);
+    if (prefill_is_faster(a, p.kb)) return run_prefill<Tout>(a, p, s);
+    switch (token_columns(a.tokens)) {
+        case 16: return run_token<16, Tout>(a, p, s);
+        case 32: return run_token<32, Tout>(a, p, s);
+        default: return run_token<64, Tout>(a, p, s);
+    }
 }
 
 }  // namespace
