@@ -297,59 +297,117 @@ __global__ void __launch_bounds__(256) quantize_kernel(const T* x, uint8_t* q, f
 }
 
 // Channel-major (batch, dim, L) to token rows (batch * L, dim): a CTA takes 128 channels of 64
-// tokens through shared memory, read along the tokens and written along the channels.  Thread
-// (token, quarter) holds 32 channels of its token, so a token's 128 values are 4 threads'.
+// tokens through shared memory, read along the tokens and written along the channels.  The
+// channels' rows are copied in 16-byte vectors of the whole array (asynchronously, so that
+// six CTAs keep 110 KB an SM on the way), which a row may enter at any element: a row's first
+// token lies `shift` elements into its copy.  A thread holds 16 channels of
+// two tokens; the e4m3 values go back through shared memory, so that a token's 128 bytes are
+// stored as one line.
+// Two neighbouring elements, and the running maximum of such pairs' magnitudes.
+template <typename T> struct Pair;
+template <> struct Pair<__nv_bfloat16> {
+    __nv_bfloat162 v;
+    __device__ __forceinline__ static Pair of(__nv_bfloat16 a, __nv_bfloat16 b) { return {__nv_bfloat162(a, b)}; }
+    __device__ __forceinline__ static Pair zero() { return {__floats2bfloat162_rn(0.f, 0.f)}; }
+    __device__ __forceinline__ void max_abs(Pair w) { v = __hmax2(v, __habs2(w.v)); }
+    __device__ __forceinline__ float2 f() const { return __bfloat1622float2(v); }
+};
+template <> struct Pair<float> {
+    float2 v;
+    __device__ __forceinline__ static Pair of(float a, float b) { return {make_float2(a, b)}; }
+    __device__ __forceinline__ static Pair zero() { return {make_float2(0.f, 0.f)}; }
+    __device__ __forceinline__ void max_abs(Pair w) { v = make_float2(fmaxf(v.x, fabsf(w.v.x)), fmaxf(v.y, fabsf(w.v.y))); }
+    __device__ __forceinline__ float2 f() const { return v; }
+};
+
+// ALIGNED: rows begin at vector boundaries (L a multiple of the vector), so all shifts are zero
+// and a thread reads its two tokens of a channel at once.
 constexpr int kTok = 64;
-template <typename T>
-__global__ void __launch_bounds__(256) quantize_cm_kernel(const T* x, uint8_t* q, float* scales,
-                                                          int64_t dim, int64_t L) {
-    constexpr int kPad = 16 / sizeof(T);  // rows stay 16-byte aligned
-    __shared__ alignas(16) T tile[kGroup][kTok + kPad];
-    __shared__ float mx[4][kTok];
-    const int64_t t0 = (int64_t)blockIdx.x * kTok, c0 = (int64_t)blockIdx.y * kGroup,
-                  b = blockIdx.z;
+template <typename T, bool ALIGNED>
+__global__ void __launch_bounds__(256, sizeof(T) == 2 ? 6 : 4) quantize_cm_kernel(const T* x, uint8_t* q, float* scales,
+                                                          int64_t dim, int64_t L, int64_t total) {
+    constexpr int kVec = 16 / sizeof(T);       // elements of a copy
+    constexpr int kVecs = kTok / kVec + (ALIGNED ? 0 : 1);  // copies of a row's 64 tokens
+    constexpr int kPitch = (kTok / kVec + 1) * kVec;
+    __shared__ alignas(16) T tile[kGroup * kPitch];
+    __shared__ float2 mx[8][kTok / 2];
+    static_assert(kTok * kGroup <= (int)sizeof(tile), "the output goes where the input was");
+    const int64_t t0 = (int64_t)blockIdx.x * kTok, c0 = (int64_t)blockIdx.y * kGroup, b = blockIdx.z;
     const int nc = (int)min((int64_t)kGroup, dim - c0), nt = (int)min((int64_t)kTok, L - t0);
-    const T* src = x + (b * dim + c0) * L + t0;
-    if (L % kPad == 0) {
-        constexpr int kVecs = kTok / kPad;
-        for (int i = threadIdx.x; i < kGroup * kVecs; i += 256) {
-            const int c = i / kVecs, t = (i % kVecs) * kPad;
-            uint4 v = make_uint4(0u, 0u, 0u, 0u);
-            if (c < nc && t < nt) v = *reinterpret_cast<const uint4*>(src + (int64_t)c * L + t);
-            *reinterpret_cast<uint4*>(&tile[c][t]) = v;
+    const int64_t first = (b * dim + c0) * L + t0;  // the tile's first element
+    if (ALIGNED) {
+        const int v = threadIdx.x % kVecs;
+        const T* src = x + first + v * kVec;
+        if (v * kVec < nt)
+#pragma unroll
+            for (int c = threadIdx.x / kVecs; c < kGroup; c += 256 / kVecs)
+                if (c < nc) cp_async16(tile + c * kPitch + v * kVec, src + c * L, 16);
+    } else {
+        for (int i = threadIdx.x; i < nc * kVecs; i += 256) {
+            const int c = i / kVecs, v = i - c * kVecs;
+            const int64_t e = ((first + c * L) & ~(int64_t)(kVec - 1)) + v * kVec;
+            const int64_t left = total - e;  // elements up to the array's end
+            if (left > 0)
+                cp_async16(tile + c * kPitch + v * kVec, x + e, left < kVec ? (int)left * (int)sizeof(T) : 16);
+        }
+    }
+    cp_async_commit();
+    cp_async_wait<0>();
+    __syncthreads();
+    // two tokens of 16 channels
+    const int t = (threadIdx.x % (kTok / 2)) * 2, part = threadIdx.x / (kTok / 2);
+    Pair<T> w[16], m = Pair<T>::zero();
+    if (part * 16 < nc) {
+        const T* at = tile + part * 16 * kPitch + t;
+        const int step = (int)(L & (kVec - 1));
+        int shift = (int)((first + part * 16 * L) & (kVec - 1));
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            if (ALIGNED) {
+                w[i] = *reinterpret_cast<const Pair<T>*>(at + i * kPitch);
+            } else {
+                w[i] = Pair<T>::of(at[i * kPitch + shift], at[i * kPitch + shift + 1]);
+                shift = (shift + step) & (kVec - 1);
+            }
+            m.max_abs(w[i]);
         }
     } else {
-        for (int i = threadIdx.x; i < kGroup * kTok; i += 256) {
-            const int c = i / kTok, t = i % kTok;
-            tile[c][t] = (c < nc && t < nt) ? src[(int64_t)c * L + t] : io<T>::from_f(0.f);
-        }
+#pragma unroll
+        for (int i = 0; i < 16; ++i) w[i] = Pair<T>::zero();
+    }
+    mx[part][t / 2] = m.f();
+    __syncthreads();
+    float m0 = kAmaxFloor, m1 = kAmaxFloor;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) m0 = fmaxf(m0, mx[i][t / 2].x), m1 = fmaxf(m1, mx[i][t / 2].y);
+    const float i0 = kE4m3Max / m0, i1 = kE4m3Max / m1;
+    // piece `part` of token r at place part ^ (r / 2 % 8) of its 128 bytes: no bank conflicts
+    // where it is written (every second token) and none where it is read (whole tokens)
+    uint8_t* staged = reinterpret_cast<uint8_t*>(tile);
+    {
+        float v[16];
+        uint8_t* at = staged + t * kGroup + ((part ^ (t / 2 & 7)) * 16);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) v[i] = w[i].f().x;
+        *reinterpret_cast<uint4*>(at) = to_e4m3(v, i0);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) v[i] = w[i].f().y;
+        *reinterpret_cast<uint4*>(at + kGroup) = to_e4m3(v, i1);
+    }
+    if (part == 0) {
+        const int64_t groups = (dim + kGroup - 1) / kGroup;
+        float* sc = scales + (b * L + t0 + t) * groups + blockIdx.y;
+        if (t < nt) sc[0] = m0 / kE4m3Max;
+        if (t + 1 < nt) sc[groups] = m1 / kE4m3Max;
     }
     __syncthreads();
-    const int t = threadIdx.x % kTok, part = threadIdx.x / kTok;
-    float v[4][kE], m = 0.f;
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < kE; ++j) {
-            v[i][j] = io<T>::to_f(tile[part * 32 + i * kE + j][t]);
-            m = fmaxf(m, fabsf(v[i][j]));
-        }
-    mx[part][t] = m;
-    __syncthreads();
-    if (t >= nt) return;
-    m = fmaxf(fmaxf(fmaxf(mx[0][t], mx[1][t]), fmaxf(mx[2][t], mx[3][t])), kAmaxFloor);
-    const float inv = kE4m3Max / m;
-    const int64_t row = b * L + t0 + t;
-    uint8_t* dst = q + row * dim + c0 + part * 32;
-#pragma unroll
-    for (int i = 0; i < 4; i += 2) {
-        if (part * 32 + i * kE >= nc) break;
-#pragma unroll
-        for (int j = 0; j < kE; ++j) v[i][j] *= inv, v[i + 1][j] *= inv;
-        const uint2 lo = to_e4m3(v[i]), hi = to_e4m3(v[i + 1]);
-        *reinterpret_cast<uint4*>(dst + i * kE) = make_uint4(lo.x, lo.y, hi.x, hi.y);
+    for (int i = 0; i < 2; ++i) {
+        const int r = (threadIdx.x >> 3) + i * 32, c = threadIdx.x & 7;
+        if (r < nt && c * 16 < nc)
+            *reinterpret_cast<uint4*>(q + (b * L + t0 + r) * dim + c0 + c * 16) =
+                *reinterpret_cast<const uint4*>(staged + r * kGroup + ((c ^ (r / 2 & 7)) * 16));
     }
-    if (part == 0) scales[row * ((dim + kGroup - 1) / kGroup) + blockIdx.y] = m / kE4m3Max;
 }
 
 // Weights: a CTA per block of 128 x 128; thread (row, half) holds 64 columns of its row.
@@ -432,6 +490,17 @@ cudaError_t norm_bwd_t(const BNParams& p, cudaStream_t s) {
     return cudaGetLastError();
 }
 
+template <typename T>
+void quantize_cm(const QuantArgs& a, dim3 grid, cudaStream_t s) {
+    const T* x = static_cast<const T*>(a.x);
+    uint8_t* q = static_cast<uint8_t*>(a.q);
+    const int64_t total = a.batch * a.dim * a.seqlen;
+    if (a.seqlen % (16 / (int64_t)sizeof(T)) == 0)
+        quantize_cm_kernel<T, true><<<grid, 256, 0, s>>>(x, q, a.scales, a.dim, a.seqlen, total);
+    else
+        quantize_cm_kernel<T, false><<<grid, 256, 0, s>>>(x, q, a.scales, a.dim, a.seqlen, total);
+}
+
 }  // namespace
 
 int64_t norm_bwd_blocks(int64_t rows, int64_t dim) {
@@ -479,10 +548,8 @@ cudaError_t launch_fp8_quantize(const QuantArgs& a, cudaStream_t s) {
         return cudaGetLastError();
     }
     const dim3 grid((unsigned)((a.seqlen + kTok - 1) / kTok), (unsigned)groups, (unsigned)a.batch);
-    if (a.dtype == DType::BF16)
-        quantize_cm_kernel<<<grid, 256, 0, s>>>(static_cast<const __nv_bfloat16*>(a.x), q, a.scales, a.dim, a.seqlen);
-    else
-        quantize_cm_kernel<<<grid, 256, 0, s>>>(static_cast<const float*>(a.x), q, a.scales, a.dim, a.seqlen);
+    if (a.dtype == DType::BF16) quantize_cm<__nv_bfloat16>(a, grid, s);
+    else quantize_cm<float>(a, grid, s);
     return cudaGetLastError();
 }
 

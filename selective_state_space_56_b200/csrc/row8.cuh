@@ -110,6 +110,15 @@ __device__ __forceinline__ uint2 to_e4m3(const float (&v)[kE]) {
     return make_uint2((uint32_t)h[0] | ((uint32_t)h[1] << 16), (uint32_t)h[2] | ((uint32_t)h[3] << 16));
 }
 
+// Sixteen, each times `inv`.
+__device__ __forceinline__ uint4 to_e4m3(const float (&v)[16], float inv) {
+    float lo[kE], hi[kE];
+#pragma unroll
+    for (int j = 0; j < kE; ++j) lo[j] = v[j] * inv, hi[j] = v[kE + j] * inv;
+    const uint2 a = to_e4m3(lo), b = to_e4m3(hi);
+    return make_uint4(a.x, a.y, b.x, b.y);
+}
+
 // The scale of a block of values with largest magnitude amax, and its reciprocal.  The floor
 // keeps both finite for blocks of zeros (their e4m3 values are zero).
 constexpr float kE4m3Max = 448.f;
