@@ -489,11 +489,9 @@ typedef struct {
 } mamba_gated_dims; /* batch >= 1, dim >= 1, seqlen >= 0 */
 
 /*
- * Bytes of workspace mamba_gated_scan_fwd needs (zero unless there are too few rows to
- * occupy the GPU and each is cut into segments), of the checkpoints it can record, and of
- * the workspace of mamba_gated_scan_bwd.  They depend on `dims` only; 0 for invalid dims.
+ * Bytes of the checkpoints mamba_gated_scan_fwd can record, and of the workspace of
+ * mamba_gated_scan_bwd.  They depend on `dims` only; 0 for invalid dims.
  */
-size_t mamba_gated_scan_workspace_size(mamba_gated_dims dims);
 size_t mamba_gated_scan_checkpoints_size(mamba_gated_dims dims);
 size_t mamba_gated_scan_bwd_workspace_size(mamba_gated_dims dims);
 
@@ -512,8 +510,7 @@ size_t mamba_gated_scan_bwd_workspace_size(mamba_gated_dims dims);
 int mamba_gated_scan_fwd(const void* x, const void* gate, const float* gate_bias, const void* z,
                          const float* initial_state, void* y, float* last_state,
                          float* checkpoints, size_t checkpoint_bytes, mamba_gated_dims dims,
-                         mamba_dtype in_dtype, mamba_dtype out_dtype, void* workspace,
-                         size_t workspace_bytes, unsigned flags, void* stream);
+                         mamba_dtype in_dtype, mamba_dtype out_dtype, unsigned flags, void* stream);
 
 /*
  * Gradients of sum y dy + sum last_state dlast_state for mamba_gated_scan_fwd with the same

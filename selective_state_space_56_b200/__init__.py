@@ -24,7 +24,6 @@ from .ops import (  # noqa: F401
     gated_scan_bwd_workspace_size,
     gated_scan_checkpoints_size,
     gated_scan_fwd,
-    gated_scan_workspace_size,
     gated_state_update,
     load_library,
     selective_scan_bwd,

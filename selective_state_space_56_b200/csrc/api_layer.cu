@@ -34,27 +34,20 @@ constexpr int64_t kMaxBlocks = 0x7fffffff;
 
 bool gated_dims_ok(const mamba_gated_dims& d) {
     if (d.batch < 1 || d.dim < 1 || d.seqlen < 0 || !fits(d.batch, d.dim, d.seqlen + 512)) return false;
-    const int64_t rows = d.batch * d.dim;
-    int64_t nseg = 1, chunks = 0;
-    s6::gated_plan(rows, d.seqlen, &nseg, &chunks);
-    return rows <= kMaxBlocks && rows * nseg / 4 < kMaxBlocks;
+    return d.batch * d.dim <= kMaxBlocks / 8;  // CTAs of a launch
 }
 
 int64_t round256(int64_t bytes) { return (bytes + 255) / 256 * 256; }
 
-int64_t agg_bytes(const mamba_gated_dims& d) {
-    int64_t nseg = 1, chunks = 0;
-    s6::gated_plan(d.batch * d.dim, d.seqlen, &nseg, &chunks);
-    return nseg > 1 ? round256(d.batch * d.dim * nseg * 8) : 0;
+// Partial sums of the bias' gradient: one per row and CTA of the team that walks it.
+int64_t bias_bytes(const mamba_gated_dims& d) {
+    const int64_t rows = d.batch * d.dim;
+    return round256(rows * s6::gated_team(rows, d.seqlen, true).ctas * 4);
 }
 
 }  // namespace
 
 extern "C" {
-
-size_t mamba_gated_scan_workspace_size(mamba_gated_dims dims) {
-    return gated_dims_ok(dims) ? (size_t)agg_bytes(dims) : 0;
-}
 
 size_t mamba_gated_scan_checkpoints_size(mamba_gated_dims dims) {
     if (!gated_dims_ok(dims)) return 0;
@@ -63,27 +56,21 @@ size_t mamba_gated_scan_checkpoints_size(mamba_gated_dims dims) {
 
 size_t mamba_gated_scan_bwd_workspace_size(mamba_gated_dims dims) {
     if (!gated_dims_ok(dims) || dims.seqlen == 0) return 0;
-    int64_t nseg = 1, chunks = 0;
-    s6::gated_plan(dims.batch * dims.dim, dims.seqlen, &nseg, &chunks);
-    return (size_t)(agg_bytes(dims) + round256(dims.batch * dims.dim * nseg * 4)) +
-           mamba_gated_scan_checkpoints_size(dims);
+    return (size_t)bias_bytes(dims) + mamba_gated_scan_checkpoints_size(dims);
 }
 
 int mamba_gated_scan_fwd(const void* x, const void* gate, const float* gate_bias, const void* z,
                          const float* initial_state, void* y, float* last_state,
                          float* checkpoints, size_t checkpoint_bytes, mamba_gated_dims dims,
-                         mamba_dtype in_dtype, mamba_dtype out_dtype, void* workspace,
-                         size_t workspace_bytes, unsigned flags, void* stream) {
+                         mamba_dtype in_dtype, mamba_dtype out_dtype, unsigned flags, void* stream) {
     if (flags & ~MAMBA_FLAG_GIVEN_DECAY) return MAMBA_ERR_FLAGS;
     if (dims.seqlen != 0 && (!x || !gate || !y)) return MAMBA_ERR_NULL;
     if (!dtype_ok(in_dtype) || !dtype_ok(out_dtype)) return MAMBA_ERR_DTYPE;
     if (!gated_dims_ok(dims)) return MAMBA_ERR_DIMS;
-    if (!all_aligned({x, gate, gate_bias, z, initial_state, y, last_state, checkpoints, workspace}))
+    if (!all_aligned({x, gate, gate_bias, z, initial_state, y, last_state, checkpoints}))
         return MAMBA_ERR_ALIGN;
     if (checkpoints && checkpoint_bytes < mamba_gated_scan_checkpoints_size(dims))
         return MAMBA_ERR_WORKSPACE;
-    const size_t need = mamba_gated_scan_workspace_size(dims);
-    if (need > 0 && (!workspace || workspace_bytes < need)) return MAMBA_ERR_WORKSPACE;
     s6::GatedArgs a{};
     a.x = x;
     a.gate = gate;
@@ -99,7 +86,6 @@ int mamba_gated_scan_fwd(const void* x, const void* gate, const float* gate_bias
     a.given_decay = (flags & MAMBA_FLAG_GIVEN_DECAY) ? 1 : 0;
     a.in_dtype = to_dtype(in_dtype);
     a.out_dtype = to_dtype(out_dtype);
-    a.agg = need > 0 ? static_cast<float2*>(workspace) : nullptr;
     return cuda_status(s6::launch_gated_scan(a, static_cast<cudaStream_t>(stream)));
 }
 
@@ -125,26 +111,22 @@ int mamba_gated_scan_bwd(const void* x, const void* gate, const float* gate_bias
     if (checkpoints && checkpoint_bytes < ck_bytes) return MAMBA_ERR_WORKSPACE;
     const size_t need = mamba_gated_scan_bwd_workspace_size(dims);
     if (need > 0 && (!workspace || workspace_bytes < need)) return MAMBA_ERR_WORKSPACE;
-    int64_t nseg = 1, chunks = 0;
-    const int64_t rows = dims.batch * dims.dim;
-    s6::gated_plan(rows, dims.seqlen, &nseg, &chunks);
     uint8_t* ws = static_cast<uint8_t*>(workspace);
     s6::GatedArgs a{};
     a.x = x;
     a.gate = gate;
     a.gate_bias = gate_bias;
     a.h0 = initial_state;
-    a.rows = rows;
+    a.rows = dims.batch * dims.dim;
     a.dim = dims.dim;
     a.L = dims.seqlen;
     a.given_decay = decay ? 1 : 0;
     a.in_dtype = a.out_dtype = to_dtype(dtype);
-    a.agg = reinterpret_cast<float2*>(ws);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     if (checkpoints || empty) {
         a.ckpt = const_cast<float*>(checkpoints);
     } else {  // the states entering every chunk, by a forward pass without outputs
-        a.ckpt = reinterpret_cast<float*>(ws + agg_bytes(dims) + round256(rows * nseg * 4));
+        a.ckpt = reinterpret_cast<float*>(ws + bias_bytes(dims));
         const cudaError_t e = s6::launch_gated_scan(a, st);
         if (e != cudaSuccess) return cuda_status(e);
     }
@@ -157,7 +139,7 @@ int mamba_gated_scan_bwd(const void* x, const void* gate, const float* gate_bias
     g.dz = dz;
     g.dbias = dgate_bias;
     g.dh0 = dinitial_state;
-    g.bias_part = reinterpret_cast<float*>(ws + (empty ? 0 : agg_bytes(dims)));
+    g.bias_part = reinterpret_cast<float*>(ws);
     return cuda_status(s6::launch_gated_scan_bwd(a, g, st));
 }
 

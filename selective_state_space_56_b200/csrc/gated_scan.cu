@@ -24,9 +24,12 @@
 // belong to the neighbouring rows (their transformation is the identity) and store the rest
 // element by element.
 //
-// Few rows leave most of the machine idle, so then each row is cut into segments, a warp
-// each: one launch composes every segment, a second walks them from their true starts, which
-// each warp forms itself from the compositions before its own.
+// Few rows leave most of the machine idle with a warp each, so then a row is walked by all warps
+// of a CTA, or of a cluster of CTAs, side by side: each takes one of the next chunks, the
+// chunks' compositions are scanned over the warps (shared memory) and over the CTAs
+// (distributed shared memory), and every array is still read once.  (Cutting rows into segments
+// that are first composed and then walked reads x and gate twice: 126 us against FIXME us for
+// (1, 60, 524287) fp32.)
 #include <algorithm>
 
 #include "layer_launch.h"
@@ -36,7 +39,9 @@ namespace s6 {
 namespace {
 
 static_assert(kE == kGatedLane, "a lane takes one vector");
-constexpr int kWarps = 4;  // per CTA
+constexpr int kWarps = 4;     // per CTA where a warp walks a row by itself
+constexpr int kTeamWarps = 16;  // at most, per CTA where warps walk a row together
+constexpr int kMaxTeam = 8;     // CTAs of a cluster that walk a row together
 constexpr unsigned kFull = 0xffffffffu;
 
 // sigmoid(v) with the argument given as -v log2(e).
@@ -96,57 +101,119 @@ struct FParams {
     void* y;
     float* last;
     float* ck;
-    const float2* agg;
-    float2* agg_out;
-    int64_t rows, dim, L, maxch, nseg, seg_chunks;
+    int64_t rows, dim, L, maxch;
 };
 
-// The state entering segment `seg` of row r: h0 through the compositions of the segments
-// before it, 32 at a time.
-__device__ __forceinline__ float enter_forward(const float2* agg, float h, int64_t seg, int lane) {
-    for (int64_t s0 = 0; s0 < seg; s0 += 32) {
-        float P = 1.f, H = 0.f;
-        if (s0 + lane < seg) {
-            const float2 v = agg[s0 + lane];
-            P = v.x, H = v.y;
-        }
-        scan_up(P, H, lane);
-        h = fmaf(__shfl_sync(kFull, P, 31), h, __shfl_sync(kFull, H, 31));
-    }
-    return h;
+// What the warps that walk a row together hand each other, twice (a round's is read while the
+// next one's is written).
+struct Team {
+    float2 warp[2][kTeamWarps];
+    float2 cta[2][kMaxTeam];
+};
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ uint32_t cluster_ctas() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.aligned;\nbarrier.cluster.wait.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void peer_store(const float2* local, uint32_t rank, float2 v) {
+    uint32_t a;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_addr(local)), "r"(rank));
+    asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(a), "f"(v.x), "f"(v.y) : "memory");
 }
 
-// MODE 0: outputs (y unless null, last state, checkpoints).  MODE 1: the composition of the
-// warp's segment only.
-template <typename Tin, typename Tout, bool DECAY, bool GATED, int MODE>
-__global__ void __launch_bounds__(32 * kWarps) gated_fwd_kernel(const FParams p) {
-    const int lane = threadIdx.x & 31;
-    const int64_t unit = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
-    if (unit >= p.rows * p.nseg) return;
-    const int64_t r = unit / p.nseg, seg = unit - r * p.nseg;
+// One level of a team's scan: item `me` of n compositions, in order (FORWARD) or from the last
+// one back.  Passes `carry` through the items before `me` into `in`, and through all into carry.
+template <bool FORWARD>
+__device__ __forceinline__ void through(const float2* items, int n, int me, int lane, float carry_in, float& in,
+                                        float& out) {
+    float P = 1.f, H = 0.f;
+    if (lane < n) {
+        const float2 v = items[lane];
+        P = v.x, H = v.y;
+    }
+    if (FORWARD) scan_up(P, H, lane);
+    else scan_down(P, H, lane);
+    const int before = FORWARD ? me - 1 : me + 1, last = FORWARD ? n - 1 : 0;
+    const float Pb = __shfl_sync(kFull, P, before & 31), Hb = __shfl_sync(kFull, H, before & 31);
+    const float Pa = __shfl_sync(kFull, P, last), Ha = __shfl_sync(kFull, H, last);
+    in = (FORWARD ? me > 0 : me + 1 < n) ? fmaf(Pb, carry_in, Hb) : carry_in;
+    out = fmaf(Pa, carry_in, Ha);
+}
+
+// A round of a team: this warp's composition (P, H) of its chunk; returns the value entering the
+// chunk and moves the row's carry past the round's chunks.
+template <bool FORWARD>
+__device__ __forceinline__ float team_round(Team& team, int buf, int ctas, int rank, float P, float H, float& carry) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+    if (lane == 0) team.warp[buf][warp] = make_float2(P, H);
+    __syncthreads();
+    float in, out;
+    if (ctas == 1) {
+        through<FORWARD>(team.warp[buf], warps, warp, lane, carry, in, out);
+        carry = out;
+        return in;
+    }
+    // the CTA's own composition, for its peers; then the carry entering this CTA's chunks
+    if (warp == 0) {
+        float Pw = 1.f, Hw = 0.f;
+        if (lane < warps) {
+            const float2 v = team.warp[buf][lane];
+            Pw = v.x, Hw = v.y;
+        }
+        if (FORWARD) scan_up(Pw, Hw, lane);
+        else scan_down(Pw, Hw, lane);
+        const int last = FORWARD ? warps - 1 : 0;
+        const float2 all = make_float2(__shfl_sync(kFull, Pw, last), __shfl_sync(kFull, Hw, last));
+        if (lane < ctas) peer_store(&team.cta[buf][rank], (uint32_t)lane, all);
+    }
+    __syncwarp();
+    cluster_sync();
+    float cta_in;
+    through<FORWARD>(team.cta[buf], ctas, rank, lane, carry, cta_in, out);
+    carry = out;
+    through<FORWARD>(team.warp[buf], warps, warp, lane, cta_in, in, out);
+    return in;
+}
+
+// TEAM: the row's chunks go round the warps of the CTA (and of its cluster); otherwise a warp
+// walks its row alone.  p.y may be null: states (checkpoints, last state) only.
+template <typename Tin, typename Tout, bool DECAY, bool GATED, bool TEAM>
+__global__ void __launch_bounds__(TEAM ? 32 * kTeamWarps : 32 * kWarps, TEAM ? 2 : 1) gated_fwd_kernel(const FParams p) {
+    __shared__ Team team;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int ctas = TEAM ? (int)cluster_ctas() : 1, rank = TEAM ? (int)cluster_rank() : 0;
+    const int64_t r = TEAM ? blockIdx.x / ctas : (int64_t)blockIdx.x * kWarps + warp;
+    if (!TEAM && r >= p.rows) return;
+    if (TEAM && ctas > 1) cluster_sync();  // every CTA's shared memory exists
     const Row w = row_of(r, p.rows, p.L);
-    const int64_t c0 = seg * p.seg_chunks;
-    const int64_t c1 = min((w.vectors + 31) / 32, c0 + p.seg_chunks);
+    const int64_t chunks = (w.vectors + 31) / 32;
+    const int64_t step = TEAM ? (int64_t)ctas * (blockDim.x >> 5) : 1;  // chunks of a round
     const float nbias = p.bias ? -kLog2e * __ldg(p.bias + r % p.dim) : 0.f;
-    float h = 0.f, Pall = 1.f;
-    if (MODE == 0) {
-        h = p.h0 ? __ldg(p.h0 + r) : 0.f;
-        if (seg > 0) h = enter_forward(p.agg + r * p.nseg, h, seg, lane);
-    }
+    float h = p.h0 ? __ldg(p.h0 + r) : 0.f;  // the state entering the round
+    int64_t c = TEAM ? (int64_t)rank * (blockDim.x >> 5) + warp : 0;
+    int64_t e = w.base + c * kGatedChunk + lane * kE;
     Raw8<Tin> xr, gr, zr, xn, gn, zn;
-    int64_t e = w.base + c0 * kGatedChunk + lane * kE;
-    if (c0 < c1) {
-        fetch<Tin>(xn, p.x, e, w);
-        fetch<Tin>(gn, p.g, e, w);
-        if (GATED) fetch<Tin>(zn, p.z, e, w);
-    }
-    for (int64_t c = c0; c < c1; ++c, e += kGatedChunk) {
+    fetch<Tin>(xn, p.x, e, w);
+    fetch<Tin>(gn, p.g, e, w);
+    if (GATED) fetch<Tin>(zn, p.z, e, w);
+    int buf = 0;
+    // every warp of a team makes every round (its chunk may lie past the row: the identity)
+    for (int64_t c_round = 0; c_round < chunks; c_round += step, c += step, e += step * kGatedChunk, buf ^= 1) {
         xr = xn, gr = gn;
         if (GATED) zr = zn;
-        if (c + 1 < c1) {
-            fetch<Tin>(xn, p.x, e + kGatedChunk, w);
-            fetch<Tin>(gn, p.g, e + kGatedChunk, w);
-            if (GATED) fetch<Tin>(zn, p.z, e + kGatedChunk, w);
+        if (c_round + step < chunks) {
+            fetch<Tin>(xn, p.x, e + step * kGatedChunk, w);
+            fetch<Tin>(gn, p.g, e + step * kGatedChunk, w);
+            if (GATED) fetch<Tin>(zn, p.z, e + step * kGatedChunk, w);
         }
         float x[kE], g[kE], a[kE], b[kE];
         xr.to_f(x);
@@ -160,12 +227,19 @@ __global__ void __launch_bounds__(32 * kWarps) gated_fwd_kernel(const FParams p)
         }
         scan_up(P, H, lane);
         const float P31 = __shfl_sync(kFull, P, 31), H31 = __shfl_sync(kFull, H, 31);
-        if (MODE == 0) {
-            if (p.ck && lane == 0) p.ck[r * p.maxch + c] = h;
-            float Pe = __shfl_up_sync(kFull, P, 1), He = __shfl_up_sync(kFull, H, 1);
-            if (lane == 0) Pe = 1.f, He = 0.f;
+        float Pe = __shfl_up_sync(kFull, P, 1), He = __shfl_up_sync(kFull, H, 1);
+        if (lane == 0) Pe = 1.f, He = 0.f;
+        float in;  // the state entering the warp's chunk
+        if (TEAM) {
+            in = team_round<true>(team, buf, ctas, rank, P31, H31, h);
+        } else {
+            in = h;
+            h = fmaf(P31, h, H31);
+        }
+        if (c < chunks) {
+            if (p.ck && lane == 0) p.ck[r * p.maxch + c] = in;
             if (p.y) {
-                float hv = fmaf(Pe, h, He);
+                float hv = fmaf(Pe, in, He);
                 float out[kE], z[kE];
                 if (GATED) zr.to_f(z);
 #pragma unroll
@@ -175,16 +249,9 @@ __global__ void __launch_bounds__(32 * kWarps) gated_fwd_kernel(const FParams p)
                 }
                 put<Tout>(p.y, e, w, out);
             }
-        } else {
-            Pall *= P31;
         }
-        h = fmaf(P31, h, H31);
     }
-    if (MODE == 1) {
-        if (lane == 0) p.agg_out[r * p.nseg + seg] = make_float2(Pall, h);
-    } else if (p.last && seg == p.nseg - 1 && lane == 0) {
-        p.last[r] = h;
-    }
+    if (p.last && lane == 0 && (!TEAM || (warp == 0 && rank == 0))) p.last[r] = h;
 }
 
 struct RParams {
@@ -195,69 +262,52 @@ struct RParams {
     void* dg;
     void* dz;
     float* dh0;
-    float* bias_part;
+    float* bias_part;  // (rows, CTAs of a team)
 };
-
-// The adjoint entering segment `seg` of row r from its right: dlast through the
-// compositions of the segments after it.
-__device__ __forceinline__ float enter_backward(const float2* agg, float e, int64_t seg,
-                                                int64_t nseg, int lane) {
-    for (int64_t s1 = nseg; s1 > seg + 1; s1 -= 32) {  // lane l holds segment s1 - 32 + l
-        float P = 1.f, E = 0.f;
-        const int64_t s = s1 - 32 + lane;
-        if (s > seg) {
-            const float2 v = agg[s];
-            P = v.x, E = v.y;
-        }
-        scan_down(P, E, lane);
-        e = fmaf(__shfl_sync(kFull, P, 0), e, __shfl_sync(kFull, E, 0));
-    }
-    return e;
-}
 
 // The backward: with e_t the adjoint handed to h_t from later steps,
 //   dh_t = dy_t silu(z_t) + e_t,  e_{t-1} = a_t dh_t,
-// the recurrence again, backwards, with the same a.  MODE 0: the gradients; a chunk's states
-// are formed again from its checkpoint.  MODE 1: the segment's composition only.
-template <typename T, bool DECAY, bool GATED, int MODE>
-__global__ void __launch_bounds__(32 * kWarps) gated_bwd_kernel(const RParams q) {
+// the recurrence again, backwards, with the same a.  A chunk's states are formed again from its
+// checkpoint, so rounds go from the row's end to its beginning and read every array once.
+template <typename T, bool DECAY, bool GATED, bool TEAM>
+__global__ void __launch_bounds__(TEAM ? 32 * kTeamWarps : 32 * kWarps) gated_bwd_kernel(const RParams q) {
+    __shared__ Team team;
+    __shared__ float sums[kTeamWarps];
     const FParams& p = q.f;
-    const int lane = threadIdx.x & 31;
-    const int64_t unit = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
-    if (unit >= p.rows * p.nseg) return;
-    const int64_t r = unit / p.nseg, seg = unit - r * p.nseg;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int ctas = TEAM ? (int)cluster_ctas() : 1, rank = TEAM ? (int)cluster_rank() : 0;
+    const int64_t r = TEAM ? blockIdx.x / ctas : (int64_t)blockIdx.x * kWarps + warp;
+    if (!TEAM && r >= p.rows) return;
+    if (TEAM && ctas > 1) cluster_sync();  // every CTA's shared memory exists
     const Row w = row_of(r, p.rows, p.L);
-    const int64_t c0 = seg * p.seg_chunks;
-    const int64_t c1 = min((w.vectors + 31) / 32, c0 + p.seg_chunks);
+    const int64_t chunks = (w.vectors + 31) / 32;
+    const int64_t step = TEAM ? (int64_t)ctas * (blockDim.x >> 5) : 1;
     const float nbias = p.bias ? -kLog2e * __ldg(p.bias + r % p.dim) : 0.f;
-    float ec = 0.f, Pall = 1.f, bsum = 0.f;
-    if (MODE == 0) {
-        ec = q.dlast ? __ldg(q.dlast + r) : 0.f;
-        if (seg + 1 < p.nseg) ec = enter_backward(p.agg + r * p.nseg, ec, seg, p.nseg, lane);
-    }
+    float ec = q.dlast ? __ldg(q.dlast + r) : 0.f, bsum = 0.f;
+    int64_t c_round = (chunks - 1) / step * step;
+    int64_t c = c_round + (TEAM ? (int64_t)rank * (blockDim.x >> 5) + warp : 0);
+    int64_t e = w.base + c * kGatedChunk + lane * kE;
     Raw8<T> xr, gr, yr, zr, xn, gn, yn, zn;
-    int64_t e = w.base + (c1 - 1) * kGatedChunk + lane * kE;
-    if (c0 < c1) {
-        if (MODE == 0) fetch<T>(xn, p.x, e, w);
-        fetch<T>(gn, p.g, e, w);
-        fetch<T>(yn, q.dy, e, w);
-        if (GATED) fetch<T>(zn, p.z, e, w);
-    }
-    for (int64_t c = c1 - 1; c >= c0; --c, e -= kGatedChunk) {
-        if (MODE == 0) xr = xn;
-        gr = gn, yr = yn;
+    float kn = c < chunks ? __ldg(p.ck + r * p.maxch + c) : 0.f;
+    fetch<T>(xn, p.x, e, w);
+    fetch<T>(gn, p.g, e, w);
+    fetch<T>(yn, q.dy, e, w);
+    if (GATED) fetch<T>(zn, p.z, e, w);
+    int buf = 0;
+    for (; c_round >= 0; c_round -= step, c -= step, e -= step * kGatedChunk, buf ^= 1) {
+        xr = xn, gr = gn, yr = yn;
         if (GATED) zr = zn;
-        if (c > c0) {
-            if (MODE == 0) fetch<T>(xn, p.x, e - kGatedChunk, w);
-            fetch<T>(gn, p.g, e - kGatedChunk, w);
-            fetch<T>(yn, q.dy, e - kGatedChunk, w);
-            if (GATED) fetch<T>(zn, p.z, e - kGatedChunk, w);
+        const float entering = kn;
+        if (c_round > 0) {
+            const int64_t en = e - step * kGatedChunk;
+            kn = __ldg(p.ck + r * p.maxch + c - step);
+            fetch<T>(xn, p.x, en, w);
+            fetch<T>(gn, p.g, en, w);
+            fetch<T>(yn, q.dy, en, w);
+            if (GATED) fetch<T>(zn, p.z, en, w);
         }
         float x[kE], g[kE], gy[kE], a[kE], b[kE], z[kE];
-        if (MODE == 0) xr.to_f(x);
-        else
-#pragma unroll
-            for (int j = 0; j < kE; ++j) x[j] = 0.f;
+        xr.to_f(x);
         gr.to_f(g);
         yr.to_f(gy);
         steps<DECAY>(x, g, nbias, e, w, a, b);
@@ -286,77 +336,85 @@ __global__ void __launch_bounds__(32 * kWarps) gated_bwd_kernel(const RParams q)
         float Pd = P;
         scan_down(Pd, E, lane);
         const float P0 = __shfl_sync(kFull, Pd, 0), E0 = __shfl_sync(kFull, E, 0);
-        if (MODE == 0) {
-            float hv[kE];  // the state before each step
-            {
-                float H = b[0];
-#pragma unroll
-                for (int j = 1; j < kE; ++j) H = fmaf(a[j], H, b[j]);
-                scan_up(P, H, lane);
-                float Pe = __shfl_up_sync(kFull, P, 1), He = __shfl_up_sync(kFull, H, 1);
-                if (lane == 0) Pe = 1.f, He = 0.f;
-                hv[0] = fmaf(Pe, __ldg(p.ck + r * p.maxch + c), He);
-#pragma unroll
-                for (int j = 1; j < kE; ++j) hv[j] = fmaf(a[j - 1], hv[j - 1], b[j - 1]);
-            }
-            if (GATED) {
-#pragma unroll
-                for (int j = 0; j < kE; ++j) dz[j] *= fmaf(a[j], hv[j], b[j]);
-                put<T>(q.dz, e, w, dz);
-            }
-            float Pe = __shfl_down_sync(kFull, Pd, 1), Ee = __shfl_down_sync(kFull, E, 1);
-            if (lane == 31) Pe = 1.f, Ee = 0.f;
-            float ev = fmaf(Pe, ec, Ee);
-            float dx[kE], dg[kE];
-#pragma unroll
-            for (int j = kE - 1; j >= 0; --j) {
-                const float dh = gy[j] + ev;
-                ev = a[j] * dh;
-                if (DECAY) {
-                    dx[j] = dh;
-                    dg[j] = dh * hv[j];
-                } else {
-                    const float s = 1.f - a[j];
-                    dx[j] = s * dh;
-                    dg[j] = dx[j] * (x[j] - hv[j]) * a[j];
-                }
-            }
-            put<T>(q.dx, e, w, dx);
-            put<T>(q.dg, e, w, dg);
-            if (!DECAY) {
-                if (edge) {
-#pragma unroll
-                    for (int j = 0; j < kE; ++j)
-                        if (e + j < w.lo || e + j >= w.hi) dg[j] = 0.f;
-                }
-                bsum += ((dg[0] + dg[1]) + (dg[2] + dg[3])) + ((dg[4] + dg[5]) + (dg[6] + dg[7]));
-            }
+        float in;  // the adjoint entering the chunk from its right
+        if (TEAM) {
+            in = team_round<false>(team, buf, ctas, rank, P0, E0, ec);
+            if (c >= chunks) continue;
         } else {
-            Pall *= P0;
+            in = ec;
+            ec = fmaf(P0, ec, E0);
         }
-        ec = fmaf(P0, ec, E0);
+        float hv[kE];  // the state before each step
+        {
+            float H = b[0];
+#pragma unroll
+            for (int j = 1; j < kE; ++j) H = fmaf(a[j], H, b[j]);
+            scan_up(P, H, lane);
+            float Pe = __shfl_up_sync(kFull, P, 1), He = __shfl_up_sync(kFull, H, 1);
+            if (lane == 0) Pe = 1.f, He = 0.f;
+            hv[0] = fmaf(Pe, entering, He);
+#pragma unroll
+            for (int j = 1; j < kE; ++j) hv[j] = fmaf(a[j - 1], hv[j - 1], b[j - 1]);
+        }
+        if (GATED) {
+#pragma unroll
+            for (int j = 0; j < kE; ++j) dz[j] *= fmaf(a[j], hv[j], b[j]);
+            put<T>(q.dz, e, w, dz);
+        }
+        float Pe = __shfl_down_sync(kFull, Pd, 1), Ee = __shfl_down_sync(kFull, E, 1);
+        if (lane == 31) Pe = 1.f, Ee = 0.f;
+        float ev = fmaf(Pe, in, Ee);
+        float dx[kE], dg[kE];
+#pragma unroll
+        for (int j = kE - 1; j >= 0; --j) {
+            const float dh = gy[j] + ev;
+            ev = a[j] * dh;
+            if (DECAY) {
+                dx[j] = dh;
+                dg[j] = dh * hv[j];
+            } else {
+                const float s = 1.f - a[j];
+                dx[j] = s * dh;
+                dg[j] = dx[j] * (x[j] - hv[j]) * a[j];
+            }
+        }
+        put<T>(q.dx, e, w, dx);
+        put<T>(q.dg, e, w, dg);
+        if (!DECAY) {
+            if (edge) {
+#pragma unroll
+                for (int j = 0; j < kE; ++j)
+                    if (e + j < w.lo || e + j >= w.hi) dg[j] = 0.f;
+            }
+            bsum += ((dg[0] + dg[1]) + (dg[2] + dg[3])) + ((dg[4] + dg[5]) + (dg[6] + dg[7]));
+        }
     }
-    if (MODE == 1) {
-        if (lane == 0) const_cast<float2*>(p.agg)[r * p.nseg + seg] = make_float2(Pall, ec);
-        return;
-    }
-    if (q.dh0 && seg == 0 && lane == 0) q.dh0[r] = ec;
+    if (q.dh0 && lane == 0 && (!TEAM || (warp == 0 && rank == 0))) q.dh0[r] = ec;
     if (q.bias_part) {
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) bsum += __shfl_xor_sync(kFull, bsum, o);
-        if (lane == 0) q.bias_part[r * p.nseg + seg] = bsum;
+        if (TEAM) {
+            if (lane == 0) sums[warp] = bsum;
+            __syncthreads();
+            if (threadIdx.x == 0) {
+                for (int i = 1; i < (int)(blockDim.x >> 5); ++i) bsum += sums[i];
+                q.bias_part[r * ctas + rank] = bsum;
+            }
+        } else if (lane == 0) {
+            q.bias_part[r] = bsum;
+        }
     }
 }
 
 // dbias[d]: the partial sums of channel d's rows, in a fixed order (a warp per channel).
 __global__ void gated_bias_kernel(const float* part, float* dbias, int64_t batch, int64_t dim,
-                                  int64_t nseg) {
+                                  int64_t parts) {
     const int lane = threadIdx.x & 31;
     const int64_t d = (int64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
     if (d >= dim) return;
     float v = 0.f;
-    for (int64_t i = lane; i < batch * nseg; i += 32)
-        v += part[((i / nseg) * dim + d) * nseg + i % nseg];
+    for (int64_t i = lane; i < batch * parts; i += 32)
+        v += part[((i / parts) * dim + d) * parts + i % parts];
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(kFull, v, o);
     if (lane == 0) dbias[d] = v;
@@ -392,8 +450,6 @@ __global__ void __launch_bounds__(128) gated_update_kernel(float* state, const T
     *reinterpret_cast<TV*>(y + i) = yv;
 }
 
-unsigned warp_blocks(int64_t units) { return (unsigned)((units + kWarps - 1) / kWarps); }
-
 FParams fparams(const GatedArgs& a) {
     FParams p;
     p.x = a.x;
@@ -404,26 +460,40 @@ FParams fparams(const GatedArgs& a) {
     p.y = a.y;
     p.last = a.last_state;
     p.ck = a.ckpt;
-    p.agg = a.agg;
-    p.agg_out = a.agg;
     p.rows = a.rows;
     p.dim = a.dim;
     p.L = a.L;
     p.maxch = gated_chunks(a.L);
-    gated_plan(a.rows, a.L, &p.nseg, &p.seg_chunks);
     return p;
+}
+
+// Launches `alone` with a warp per row, or `team` with the plan's warps and CTAs per row.
+template <typename Params>
+cudaError_t launch_rows(void (*alone)(Params), void (*team)(Params), const Params& p, int64_t rows,
+                        const GatedTeam& t, cudaStream_t s) {
+    if (t.warps * t.ctas == 1) {
+        alone<<<(unsigned)((rows + kWarps - 1) / kWarps), 32 * kWarps, 0, s>>>(p);
+        return cudaGetLastError();
+    }
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(rows * t.ctas));
+    cfg.blockDim = dim3((unsigned)(32 * t.warps));
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = (unsigned)t.ctas;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, team, p);
 }
 
 template <typename Tin, typename Tout, bool DECAY, bool GATED>
 cudaError_t run_fwd(const FParams& p, cudaStream_t s) {
-    const unsigned blocks = warp_blocks(p.rows * p.nseg);
-    if (p.nseg > 1) {
-        gated_fwd_kernel<Tin, Tin, DECAY, false, 1><<<blocks, 32 * kWarps, 0, s>>>(p);
-        const cudaError_t e = cudaGetLastError();
-        if (e != cudaSuccess) return e;
-    }
-    gated_fwd_kernel<Tin, Tout, DECAY, GATED, 0><<<blocks, 32 * kWarps, 0, s>>>(p);
-    return cudaGetLastError();
+    return launch_rows(gated_fwd_kernel<Tin, Tout, DECAY, GATED, false>,
+                       gated_fwd_kernel<Tin, Tout, DECAY, GATED, true>, p, p.rows,
+                       gated_team(p.rows, p.L, false), s);
 }
 template <typename Tin, typename Tout>
 cudaError_t run_fwd_t(const FParams& p, bool decay, cudaStream_t s) {
@@ -434,14 +504,8 @@ cudaError_t run_fwd_t(const FParams& p, bool decay, cudaStream_t s) {
 
 template <typename T, bool DECAY, bool GATED>
 cudaError_t run_bwd(const RParams& q, cudaStream_t s) {
-    const unsigned blocks = warp_blocks(q.f.rows * q.f.nseg);
-    if (q.f.nseg > 1) {
-        gated_bwd_kernel<T, DECAY, GATED, 1><<<blocks, 32 * kWarps, 0, s>>>(q);
-        const cudaError_t e = cudaGetLastError();
-        if (e != cudaSuccess) return e;
-    }
-    gated_bwd_kernel<T, DECAY, GATED, 0><<<blocks, 32 * kWarps, 0, s>>>(q);
-    return cudaGetLastError();
+    return launch_rows(gated_bwd_kernel<T, DECAY, GATED, false>, gated_bwd_kernel<T, DECAY, GATED, true>, q,
+                       q.f.rows, gated_team(q.f.rows, q.f.L, true), s);
 }
 template <typename T>
 cudaError_t run_bwd_t(const RParams& q, bool decay, cudaStream_t s) {
@@ -469,13 +533,21 @@ cudaError_t run_update(const GatedUpdateArgs& a, cudaStream_t s) {
 
 }  // namespace
 
-void gated_plan(int64_t rows, int64_t L, int64_t* nseg, int64_t* seg_chunks) {
-    const int64_t chunks = std::max<int64_t>(1, gated_chunks(L));
-    int64_t n = 1;
-    constexpr int64_t kEnough = 148 * 16, kTarget = 148 * 32, kLeast = 4;
-    if (rows < kEnough) n = std::min((kTarget + rows - 1) / rows, (chunks + kLeast - 1) / kLeast);
-    *seg_chunks = (chunks + n - 1) / n;
-    *nseg = (chunks + *seg_chunks - 1) / *seg_chunks;
+// Warps that walk a row: one while the rows alone give every SM `per_sm` of them (32 forward, 16
+// for the backward's larger register need); else as many as bring it there, in one CTA, or in a
+// cluster of up to 8 where there are fewer rows than CTA places; never more than the row has chunks.
+GatedTeam gated_team(int64_t rows, int64_t L, bool backward) {
+    constexpr int64_t kSms = 148;
+    const int64_t per_sm = backward ? 16 : 32, chunks = std::max<int64_t>(1, gated_chunks(L));
+    const int64_t ctas_per_sm = (rows + kSms - 1) / kSms;
+    GatedTeam t{1, 1};
+    const int64_t warps = std::min<int64_t>({kTeamWarps, per_sm / std::min(ctas_per_sm, per_sm), chunks});
+    if (warps <= 1) return t;
+    t.warps = (int)warps;
+    if (warps == kTeamWarps)
+        t.ctas = (int)std::max<int64_t>(1, std::min<int64_t>({kMaxTeam, kSms * per_sm / kTeamWarps / rows,
+                                                              (chunks + kTeamWarps - 1) / kTeamWarps}));
+    return t;
 }
 
 cudaError_t launch_gated_scan(const GatedArgs& a, cudaStream_t s) {
@@ -516,7 +588,8 @@ cudaError_t launch_gated_scan_bwd(const GatedArgs& a, const GatedBwdArgs& g, cud
                                               : run_bwd_t<float>(q, a.given_decay != 0, s);
     if (e == cudaSuccess && g.dbias) {
         gated_bias_kernel<<<(unsigned)((a.dim + 3) / 4), 128, 0, s>>>(g.bias_part, g.dbias,
-                                                                     a.rows / a.dim, a.dim, q.f.nseg);
+                                                                     a.rows / a.dim, a.dim,
+                                                                     gated_team(a.rows, a.L, true).ctas);
         e = cudaGetLastError();
     }
     return e;

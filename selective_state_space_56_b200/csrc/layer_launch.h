@@ -20,9 +20,12 @@ inline int64_t gated_chunks(int64_t L) {
     return L > 0 ? (L + (kGatedLane - 1) + (kGatedChunk - 1)) / kGatedChunk : 0;
 }
 
-// Split of every row into nseg segments of seg_chunks chunks, walked by a warp each
-// (nseg = 1: a warp walks a whole row).  Depends on the sizes alone.
-void gated_plan(int64_t rows, int64_t L, int64_t* nseg, int64_t* seg_chunks);
+// Warps of a CTA and CTAs of a cluster that walk a row together (1, 1: a warp by itself).
+// Depends on the sizes alone.
+struct GatedTeam {
+    int warps, ctas;
+};
+GatedTeam gated_team(int64_t rows, int64_t L, bool backward);
 
 struct GatedArgs {
     const void* x;     // (rows, L) in_dtype
@@ -36,7 +39,6 @@ struct GatedArgs {
     int64_t rows, dim, L;
     int given_decay;
     DType in_dtype, out_dtype;
-    float2* agg;  // (rows, nseg) when the plan splits
 };
 
 struct GatedBwdArgs {
@@ -47,7 +49,7 @@ struct GatedBwdArgs {
     void* dz;             // (rows, L) in_dtype, null without z
     float* dbias;         // (dim), null without a bias
     float* dh0;           // (rows) or null
-    float* bias_part;     // (rows, nseg) partial sums of dgate, when dbias
+    float* bias_part;     // (rows, CTAs of the backward's team) partial sums of dgate, when dbias
 };
 
 cudaError_t launch_gated_scan(const GatedArgs& a, cudaStream_t stream);

@@ -105,13 +105,13 @@ def load_library():
             lib.mamba_selective_state_update.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, vp, i32,
                                                          vp, i64, i64, i64, i32, vp]
             size, f32 = ctypes.c_size_t, ctypes.c_float
-            for name in ("workspace", "checkpoints", "bwd_workspace"):
+            for name in ("checkpoints", "bwd_workspace"):
                 fn = getattr(lib, "mamba_gated_scan_%s_size" % name)
                 fn.restype, fn.argtypes = size, [GatedDims]
             lib.mamba_add_rms_norm_bwd_workspace_size.restype = size
             lib.mamba_add_rms_norm_bwd_workspace_size.argtypes = [i64, i64]
             for name, args in (
-                    ("gated_scan_fwd", [vp] * 8 + [size, GatedDims, i32, i32, vp, size, u32, vp]),
+                    ("gated_scan_fwd", [vp] * 8 + [size, GatedDims, i32, i32, u32, vp]),
                     ("gated_scan_bwd", [vp] * 13 + [size, GatedDims, i32, vp, size, u32, vp]),
                     ("gated_state_update", [vp] * 6 + [i64, i64, i32, u32, vp]),
                     ("add_rms_norm_fwd", [vp] * 3 + [f32, vp, vp, i64, i64, i32, i32, i32, vp]),
@@ -647,11 +647,6 @@ def _run(name, dev, *args):
         raise MambaError(rc, name)
 
 
-def gated_scan_workspace_size(batch: int, dim: int, seqlen: int) -> int:
-    """Bytes of workspace ``gated_scan_fwd`` needs for these sizes (0 if none)."""
-    return int(load_library().mamba_gated_scan_workspace_size(GatedDims(batch, dim, seqlen)))
-
-
 def gated_scan_checkpoints_size(batch: int, dim: int, seqlen: int) -> int:
     """Bytes of the checkpoints ``gated_scan_fwd`` can record for ``gated_scan_bwd``."""
     return int(load_library().mamba_gated_scan_checkpoints_size(GatedDims(batch, dim, seqlen)))
@@ -671,7 +666,7 @@ def _workspace(workspace, need, like, dev):
 
 def gated_scan_fwd(x, gate, gate_bias=None, z=None, initial_state=None, given_decay=False,
                    out_dtype=None, y=None, last_state=None, return_last_state=False,
-                   checkpoints=None, workspace=None):
+                   checkpoints=None):
     """Gated linear recurrence h_t = (1 - s_t) h_{t-1} + s_t x_t with s_t = sigmoid(gate_t +
     gate_bias), or h_t = gate_t h_{t-1} + x_t with given_decay; y_t = h_t silu(z_t) (h_t
     without z).  x, gate, z: (batch, dim, L); gate_bias: (dim) fp32; initial_state: (batch,
@@ -688,13 +683,10 @@ def gated_scan_fwd(x, gate, gate_bias=None, z=None, initial_state=None, given_de
     if last_state is not None or return_last_state:
         last_state, lp = _output(last_state, "last_state", x, dev, (b, d), f32)
     ck, ck_bytes = _buffer(checkpoints, "checkpoints", dev)
-    dims = GatedDims(b, d, L)
-    need = (_lib or load_library()).mamba_gated_scan_workspace_size(dims)
-    workspace, ws, ws_bytes = _workspace(workspace, need, x, dev)
     _run("mamba_gated_scan_fwd", dev, x.data_ptr(), _is(gate, "gate", dev, shape, in_dt),
          _maybe(gate_bias, "gate_bias", dev, (d,), f32), _maybe(z, "z", dev, shape, in_dt),
-         _maybe(initial_state, "initial_state", dev, (b, d), f32), yp, lp, ck, ck_bytes, dims, in_code, out_code, ws,
-         ws_bytes, MAMBA_FLAG_GIVEN_DECAY if given_decay else 0)
+         _maybe(initial_state, "initial_state", dev, (b, d), f32), yp, lp, ck, ck_bytes, GatedDims(b, d, L), in_code,
+         out_code, MAMBA_FLAG_GIVEN_DECAY if given_decay else 0)
     return (y, last_state) if return_last_state else y
 
 

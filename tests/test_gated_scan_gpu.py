@@ -87,19 +87,25 @@ def test_gated_scan_options(cuda_ok, decay, z, h0):
 
 
 @pytest.mark.parametrize("decay", [False, True], ids=["sigmoid", "decay"])
-def test_gated_scan_many_segments(cuda_ok, decay):
-    """Few long rows: over 32 segments, so the entering states are folded in several groups;
-    a length whose last chunk only some rows touch."""
-    assert ops.gated_scan_workspace_size(1, 3, 70001) > 0
+def test_gated_scan_few_long_rows(cuda_ok, decay):
+    """Few long rows: a cluster of CTAs walks each; a length whose last chunk only some rows
+    touch."""
     p = problem(1, 3, 70001, "fp32", decay, seed=3)
     compare(p, "fp32", decay)
     compare(p, "fp32", decay, checkpoints=False)
 
 
 def test_gated_scan_enough_rows(cuda_ok):
-    """A row per warp (no segments), rows ending inside a vector."""
-    assert ops.gated_scan_workspace_size(2, 1200, 301) == 0
+    """Rows enough for one warp each in the backward and nearly so in the forward, ending inside a
+    vector."""
     compare(problem(2, 1200, 301, "bf16", False, seed=4), "bf16", False)
+
+
+@pytest.mark.parametrize("rows", [1, 20, 75, 149, 300, 700, 2400])
+@pytest.mark.parametrize("L", [600, 5003])
+def test_gated_scan_rows_by_teams(cuda_ok, rows, L):
+    """Every way of sharing a row: clusters of 8 down to 1 CTAs, 16 down to 1 warps."""
+    compare(problem(1, rows, L, "bf16", rows % 2 == 0, seed=rows), "bf16", rows % 2 == 0)
 
 
 def test_gated_scan_gradients_against_differences(cuda_ok):
@@ -218,7 +224,6 @@ def test_gated_graphs_and_streams(cuda_ok):
     """A captured forward and backward, replayed on new inputs, equal the eager calls; two graphs
     with workspaces of their own replay side by side on two streams."""
     probs = [dev(problem(1, 40, 5000, "bf16", False, seed=s)) for s in (1, 2)]
-    assert ops.gated_scan_workspace_size(1, 40, 5000) > 0
 
     def step(c, ck):
         y, last = ops.gated_scan_fwd(c["x"], c["gate"], c["bias"], c["z"], c["h0"],

@@ -19,11 +19,11 @@ def lib():
     return ops.load_library()
 
 
-def fwd(lib, dims=(2, 3, 100), ws=None, wsb=0, ck=None, ckb=0, i=0, o=0, flags=0, **kw):
+def fwd(lib, dims=(2, 3, 100), ck=None, ckb=0, i=0, o=0, flags=0, **kw):
     a = dict(x=P, gate=P, bias=None, z=None, h0=None, y=P, last=None)
     a.update(kw)
     return lib.mamba_gated_scan_fwd(a["x"], a["gate"], a["bias"], a["z"], a["h0"], a["y"], a["last"],
-                                    ck, ckb, ops.GatedDims(*dims), i, o, ws, wsb, flags, None)
+                                    ck, ckb, ops.GatedDims(*dims), i, o, flags, None)
 
 
 def bwd(lib, dims=(2, 5000, 100), ws=P, wsb=1 << 40, ck=None, ckb=0, i=0, flags=0, **kw):
@@ -50,7 +50,6 @@ def test_gated_forward_alignment(lib, field):
 def test_gated_dims(lib, dims):
     assert fwd(lib, dims=dims) == DIMS
     assert bwd(lib, dims=dims) == DIMS
-    assert lib.mamba_gated_scan_workspace_size(ops.GatedDims(*dims)) == 0
     assert lib.mamba_gated_scan_checkpoints_size(ops.GatedDims(*dims)) == 0
     assert lib.mamba_gated_scan_bwd_workspace_size(ops.GatedDims(*dims)) == 0
 
@@ -60,12 +59,7 @@ def test_gated_other_refusals(lib):
     assert fwd(lib, flags=1) == FLAGS and bwd(lib, flags=4) == FLAGS
     need = ops.gated_scan_checkpoints_size(2, 3, 100)
     assert need > 0 and fwd(lib, ck=P, ckb=need - 1) == WORKSPACE
-    long = (1, 8, 1 << 16)
-    need = ops.gated_scan_workspace_size(*long)
-    assert need > 0 and fwd(lib, dims=long) == WORKSPACE
-    assert fwd(lib, dims=long, ws=P, wsb=need - 1) == WORKSPACE
-    assert fwd(lib, dims=long, ws=P + 4, wsb=need) == ALIGN
-    assert ops.gated_scan_workspace_size(4, 5120, 4096) == 0
+    assert fwd(lib, ck=P + 4, ckb=need) == ALIGN
 
 
 @pytest.mark.parametrize("field", ["x", "gate", "dy", "dx", "dg"])
