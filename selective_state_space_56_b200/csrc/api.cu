@@ -549,11 +549,12 @@ int mamba_diag_wait_timeout(int64_t limit_cycles, void* stream) {
 }
 
 int mamba_check_device_error(int clear, void* stream) {
-    unsigned word = 0, linear = 0;
+    unsigned word = 0, linear = 0, gated = 0;
     if (s6::read_device_error(&word, clear != 0, static_cast<cudaStream_t>(stream)) != cudaSuccess ||
-        s6::read_linear_error(&linear, clear != 0, static_cast<cudaStream_t>(stream)) != cudaSuccess)
+        s6::read_linear_error(&linear, clear != 0, static_cast<cudaStream_t>(stream)) != cudaSuccess ||
+        s6::read_gated_error(&gated, clear != 0, static_cast<cudaStream_t>(stream)) != cudaSuccess)
         return MAMBA_ERR_CUDA;
-    return word | linear ? MAMBA_ERR_TIMEOUT : MAMBA_OK;
+    return word | linear | gated ? MAMBA_ERR_TIMEOUT : MAMBA_OK;
 }
 
 const char* mamba_status_string(int status) {

@@ -32,8 +32,10 @@ bool fits(int64_t a, int64_t b, int64_t c) {
 
 constexpr int64_t kMaxBlocks = 0x7fffffff;
 
+constexpr int64_t kMaxSteps = (int64_t)1 << 38;  // a row's chunks are counted in 32 bits
+
 bool gated_dims_ok(const mamba_gated_dims& d) {
-    if (d.batch < 1 || d.dim < 1 || d.seqlen < 0 || !fits(d.batch, d.dim, d.seqlen + 512)) return false;
+    if (d.batch < 1 || d.dim < 1 || d.seqlen < 0 || d.seqlen > kMaxSteps || !fits(d.batch, d.dim, d.seqlen + 512)) return false;
     return d.batch * d.dim <= kMaxBlocks / 8;  // CTAs of a launch
 }
 

@@ -43,53 +43,77 @@ constexpr int kWarps = 4;     // per CTA where a warp walks a row by itself
 constexpr int kTeamWarps = 16;  // at most, per CTA where warps walk a row together
 constexpr int kMaxTeam = 8;     // CTAs of a cluster that walk a row together
 constexpr unsigned kFull = 0xffffffffu;
+__device__ unsigned int g_gated_error = 0;        // a bounded wait gave up
+constexpr long long kLimit = 2000000000LL;  // SM clocks, about a second
 
-// sigmoid(v) with the argument given as -v log2(e).
-__device__ __forceinline__ float sigmoid_of(float t) { return rcp(1.f + ex2(t)); }
+// sigmoid of a pair, the arguments given as -v log2(e).
+__device__ __forceinline__ f2 sigmoid2(f2 t) {
+    float d0, d1;
+    unpack2(add2(ex2x2(t), pack2(1.f, 1.f)), d0, d1);
+    return pack2(rcp(d0), rcp(d1));
+}
+__device__ __forceinline__ f2 twice(float v) { return pack2(v, v); }
 
-// The lane's 8 steps (a_j, b_j); steps outside the row become the identity.
-template <bool DECAY>
-__device__ __forceinline__ void steps(const float (&x)[kE], const float (&g)[kE], float nbias,
-                                      int64_t e, const Row& w, float (&a)[kE], float (&b)[kE]) {
+// The lane's 8 steps (a_j, b_j), two at a time in packed arithmetic; nbias = -bias log2(e).
+template <bool DECAY, typename T>
+__device__ __forceinline__ void steps(const Raw8<T>& x, const Raw8<T>& g, float nbias, float (&a)[kE],
+                                      float (&b)[kE]) {
 #pragma unroll
-    for (int j = 0; j < kE; ++j) {
-        if (DECAY) {
-            a[j] = g[j];
-            b[j] = x[j];
-        } else {
-            const float s = sigmoid_of(fmaf(g[j], -kLog2e, nbias));
-            a[j] = 1.f - s;
-            b[j] = s * x[j];
+    for (int i = 0; i < kE / 2; ++i) {
+        f2 av = g.pair(i), bv = x.pair(i);
+        if (!DECAY) {
+            const f2 s = sigmoid2(fma2(av, twice(-kLog2e), twice(nbias)));
+            av = sub2(twice(1.f), s);
+            bv = mul2(s, bv);
         }
-    }
-    if (e < w.lo || e + kE > w.hi) {
-#pragma unroll
-        for (int j = 0; j < kE; ++j)
-            if (e + j < w.lo || e + j >= w.hi) a[j] = 1.f, b[j] = 0.f;
+        unpack2(av, a[2 * i], a[2 * i + 1]);
+        unpack2(bv, b[2 * i], b[2 * i + 1]);
     }
 }
-
-// Inclusive scan over the lanes of the compositions (P, H), earlier lanes first.
-__device__ __forceinline__ void scan_up(float& P, float& H, int lane) {
+// Steps outside the row become the identity.
+__device__ __forceinline__ void mask_steps(int64_t e, const Row& w, float (&a)[kE], float (&b)[kE]) {
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const float Pp = __shfl_up_sync(kFull, P, o), Hp = __shfl_up_sync(kFull, H, o);
-        if (lane >= o) {
-            H = fmaf(P, Hp, H);
-            P *= Pp;
-        }
-    }
+    for (int j = 0; j < kE; ++j)
+        if (e + j < w.lo || e + j >= w.hi) a[j] = 1.f, b[j] = 0.f;
+}
+
+// Inclusive scan over the lanes of the compositions (P, H), earlier lanes first.  (The shuffle's
+// own predicate says which lanes have a partner.)
+__device__ __forceinline__ void scan_up(float& P, float& H) {
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1)
+        asm("{\n .reg .f32 q, r;\n .reg .pred p;\n"
+            " shfl.sync.up.b32 q|p, %0, %2, 0, 0xffffffff;\n shfl.sync.up.b32 r|p, %1, %2, 0, 0xffffffff;\n"
+            " @p fma.rn.f32 %1, %0, r, %1;\n @p mul.rn.f32 %0, %0, q;\n}\n"
+            : "+f"(P), "+f"(H)
+            : "r"(o));
 }
 // The same from the last lane down (the adjoint runs backwards in time).
-__device__ __forceinline__ void scan_down(float& P, float& E, int lane) {
+__device__ __forceinline__ void scan_down(float& P, float& H) {
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const float Pp = __shfl_down_sync(kFull, P, o), Ep = __shfl_down_sync(kFull, E, o);
-        if (lane + o < 32) {
-            E = fmaf(P, Ep, E);
-            P *= Pp;
-        }
-    }
+    for (int o = 1; o < 32; o <<= 1)
+        asm("{\n .reg .f32 q, r;\n .reg .pred p;\n"
+            " shfl.sync.down.b32 q|p, %0, %2, 31, 0xffffffff;\n shfl.sync.down.b32 r|p, %1, %2, 31, 0xffffffff;\n"
+            " @p fma.rn.f32 %1, %0, r, %1;\n @p mul.rn.f32 %0, %0, q;\n}\n"
+            : "+f"(P), "+f"(H)
+            : "r"(o));
+}
+
+// Whether chunk c of row w reaches past an end of the row.
+__device__ __forceinline__ bool at_edge(const Row& w, int c, int chunks) {
+    return (c == 0 && w.base != w.lo) || (c + 1 >= chunks && w.base + (int64_t)chunks * kGatedChunk != w.hi) ||
+           c >= chunks;
+}
+// A lane's 8 elements from e on: directly, or with the checks of an edge chunk.
+template <typename T>
+__device__ __forceinline__ void get(Raw8<T>& r, const void* p, int64_t e, const Row& w, bool edge) {
+    if (edge) fetch<T>(r, p, e, w);
+    else r.load(static_cast<const T*>(p) + e);
+}
+template <typename T>
+__device__ __forceinline__ void set(void* p, int64_t e, const Row& w, bool edge, const float (&v)[kE]) {
+    if (edge) put<T>(p, e, w, v);
+    else store_all(static_cast<T*>(p) + e, v);
 }
 
 struct FParams {
@@ -107,8 +131,11 @@ struct FParams {
 // What the warps that walk a row together hand each other, twice (a round's is read while the
 // next one's is written).
 struct Team {
-    float2 warp[2][kTeamWarps];
-    float2 cta[2][kMaxTeam];
+    float2 warp[2][kTeamWarps];    // the warps' compositions
+    float2 before[2][kTeamWarps];  // of the warps before each in the CTA
+    float enter[2];                // the value entering the CTA's chunks
+    float2 cta[2][kMaxTeam];       // the CTAs' compositions
+    uint64_t here[2];              // ... have arrived
 };
 
 __device__ __forceinline__ uint32_t cluster_rank() {
@@ -124,64 +151,78 @@ __device__ __forceinline__ uint32_t cluster_ctas() {
 __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.aligned;\nbarrier.cluster.wait.aligned;" ::: "memory");
 }
-__device__ __forceinline__ void peer_store(const float2* local, uint32_t rank, float2 v) {
-    uint32_t a;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_addr(local)), "r"(rank));
-    asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(a), "f"(v.x), "f"(v.y) : "memory");
-}
-
-// One level of a team's scan: item `me` of n compositions, in order (FORWARD) or from the last
-// one back.  Passes `carry` through the items before `me` into `in`, and through all into carry.
-template <bool FORWARD>
-__device__ __forceinline__ void through(const float2* items, int n, int me, int lane, float carry_in, float& in,
-                                        float& out) {
-    float P = 1.f, H = 0.f;
-    if (lane < n) {
-        const float2 v = items[lane];
-        P = v.x, H = v.y;
+// Sets up a cluster's hand-over; ends with every CTA's shared memory in place.
+__device__ __forceinline__ void team_begin(Team& team) {
+    if (threadIdx.x == 0) {
+        mbar_init(&team.here[0], 1);
+        mbar_init(&team.here[1], 1);
+        fence_barrier_init();
     }
-    if (FORWARD) scan_up(P, H, lane);
-    else scan_down(P, H, lane);
-    const int before = FORWARD ? me - 1 : me + 1, last = FORWARD ? n - 1 : 0;
-    const float Pb = __shfl_sync(kFull, P, before & 31), Hb = __shfl_sync(kFull, H, before & 31);
-    const float Pa = __shfl_sync(kFull, P, last), Ha = __shfl_sync(kFull, H, last);
-    in = (FORWARD ? me > 0 : me + 1 < n) ? fmaf(Pb, carry_in, Hb) : carry_in;
-    out = fmaf(Pa, carry_in, Ha);
-}
-
-// A round of a team: this warp's composition (P, H) of its chunk; returns the value entering the
-// chunk and moves the row's carry past the round's chunks.
-template <bool FORWARD>
-__device__ __forceinline__ float team_round(Team& team, int buf, int ctas, int rank, float P, float H, float& carry) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
-    if (lane == 0) team.warp[buf][warp] = make_float2(P, H);
     __syncthreads();
-    float in, out;
-    if (ctas == 1) {
-        through<FORWARD>(team.warp[buf], warps, warp, lane, carry, in, out);
-        carry = out;
-        return in;
-    }
-    // the CTA's own composition, for its peers; then the carry entering this CTA's chunks
+    cluster_sync();
+}
+// Stores v into the CTA of `rank` and counts its bytes on that CTA's barrier: what waits there is
+// ordered after this store alone (a cluster barrier would wait for the row's stores to global
+// memory too).
+__device__ __forceinline__ void hand_over(const float2* local, const uint64_t* bar, uint32_t rank, float2 v) {
+    uint32_t a, m;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_addr(local)), "r"(rank));
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(m) : "r"(smem_addr(bar)), "r"(rank));
+    asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v2.f32 [%0], {%1, %2}, [%3];" ::"r"(a),
+                 "f"(v.x), "f"(v.y), "r"(m)
+                 : "memory");
+}
+
+// A round of a team: the warp's composition of its chunk, held by lane 31 (FORWARD) or lane 0;
+// returns the value entering the chunk.  Warp 0 scans the CTA's compositions, hands its own to
+// the cluster, scans the cluster's and moves the row's carry (its alone) past the round.
+template <bool FORWARD>
+__device__ __forceinline__ float team_round(Team& team, int round, int ctas, int rank, float P, float H, float& carry,
+                                            bool& alive) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5, buf = round & 1;
+    if (lane == (FORWARD ? 31 : 0)) team.warp[buf][warp] = make_float2(P, H);
+    __syncthreads();
     if (warp == 0) {
-        float Pw = 1.f, Hw = 0.f;
+        P = 1.f, H = 0.f;
         if (lane < warps) {
             const float2 v = team.warp[buf][lane];
-            Pw = v.x, Hw = v.y;
+            P = v.x, H = v.y;
         }
-        if (FORWARD) scan_up(Pw, Hw, lane);
-        else scan_down(Pw, Hw, lane);
+        if (FORWARD) scan_up(P, H);
+        else scan_down(P, H);
         const int last = FORWARD ? warps - 1 : 0;
-        const float2 all = make_float2(__shfl_sync(kFull, Pw, last), __shfl_sync(kFull, Hw, last));
-        if (lane < ctas) peer_store(&team.cta[buf][rank], (uint32_t)lane, all);
+        const float2 all = make_float2(__shfl_sync(kFull, P, last), __shfl_sync(kFull, H, last));
+        const float Pb = FORWARD ? __shfl_up_sync(kFull, P, 1) : __shfl_down_sync(kFull, P, 1);
+        const float Hb = FORWARD ? __shfl_up_sync(kFull, H, 1) : __shfl_down_sync(kFull, H, 1);
+        const bool first = lane == (FORWARD ? 0 : warps - 1);
+        if (lane < warps) team.before[buf][lane] = first ? make_float2(1.f, 0.f) : make_float2(Pb, Hb);
+        if (ctas == 1) {
+            if (lane == 0) team.enter[buf] = carry;
+            carry = fmaf(all.x, carry, all.y);
+        } else {
+            if (lane == 0) mbar_arrive_expect_tx(&team.here[buf], (uint32_t)ctas * 8u);
+            if (lane < ctas) hand_over(&team.cta[buf][rank], &team.here[buf], (uint32_t)lane, all);
+            __syncwarp();
+            if (alive && !__all_sync(kFull, mbar_wait_bounded(&team.here[buf], (uint32_t)(round >> 1) & 1u, kLimit))) {
+                if (lane == 0) atomicOr(&g_gated_error, 1u);
+                alive = false;  // the outputs are void; the rounds end without further waits
+            }
+            P = 1.f, H = 0.f;
+            if (lane < ctas) {
+                const float2 v = team.cta[buf][lane];
+                P = v.x, H = v.y;
+            }
+            if (FORWARD) scan_up(P, H);
+            else scan_down(P, H);
+            const float after = fmaf(P, carry, H);  // this CTA's chunks and those before them
+            const float in = __shfl_sync(kFull, after, (FORWARD ? rank - 1 : rank + 1) & 31);
+            if (lane == 0) team.enter[buf] = (FORWARD ? rank > 0 : rank + 1 < ctas) ? in : carry;
+            carry = __shfl_sync(kFull, after, FORWARD ? ctas - 1 : 0);
+        }
     }
-    __syncwarp();
-    cluster_sync();
-    float cta_in;
-    through<FORWARD>(team.cta[buf], ctas, rank, lane, carry, cta_in, out);
-    carry = out;
-    through<FORWARD>(team.warp[buf], warps, warp, lane, cta_in, in, out);
-    return in;
+    __syncthreads();
+    const float2 v = team.before[buf][warp];
+    return fmaf(v.x, team.enter[buf], v.y);
 }
 
 // TEAM: the row's chunks go round the warps of the CTA (and of its cluster); otherwise a warp
@@ -193,65 +234,65 @@ __global__ void __launch_bounds__(TEAM ? 32 * kTeamWarps : 32 * kWarps, TEAM ? 2
     const int ctas = TEAM ? (int)cluster_ctas() : 1, rank = TEAM ? (int)cluster_rank() : 0;
     const int64_t r = TEAM ? blockIdx.x / ctas : (int64_t)blockIdx.x * kWarps + warp;
     if (!TEAM && r >= p.rows) return;
-    if (TEAM && ctas > 1) cluster_sync();  // every CTA's shared memory exists
+    if (TEAM && ctas > 1) team_begin(team);
     const Row w = row_of(r, p.rows, p.L);
-    const int64_t chunks = (w.vectors + 31) / 32;
-    const int64_t step = TEAM ? (int64_t)ctas * (blockDim.x >> 5) : 1;  // chunks of a round
+    const int chunks = (int)((w.vectors + 31) / 32);
+    const int step = TEAM ? ctas * (int)(blockDim.x >> 5) : 1;  // chunks of a round
     const float nbias = p.bias ? -kLog2e * __ldg(p.bias + r % p.dim) : 0.f;
     float h = p.h0 ? __ldg(p.h0 + r) : 0.f;  // the state entering the round
-    int64_t c = TEAM ? (int64_t)rank * (blockDim.x >> 5) + warp : 0;
-    int64_t e = w.base + c * kGatedChunk + lane * kE;
+    int c = TEAM ? rank * (int)(blockDim.x >> 5) + warp : 0;
+    int64_t e = w.base + (int64_t)c * kGatedChunk + lane * kE;
     Raw8<Tin> xr, gr, zr, xn, gn, zn;
-    fetch<Tin>(xn, p.x, e, w);
-    fetch<Tin>(gn, p.g, e, w);
-    if (GATED) fetch<Tin>(zn, p.z, e, w);
-    int buf = 0;
+    bool alive = true, edge, edge_n = at_edge(w, c, chunks);
+    get<Tin>(xn, p.x, e, w, edge_n);
+    get<Tin>(gn, p.g, e, w, edge_n);
+    if (GATED) get<Tin>(zn, p.z, e, w, edge_n);
     // every warp of a team makes every round (its chunk may lie past the row: the identity)
-    for (int64_t c_round = 0; c_round < chunks; c_round += step, c += step, e += step * kGatedChunk, buf ^= 1) {
-        xr = xn, gr = gn;
+    for (int c0 = 0, round = 0; c0 < chunks; c0 += step, c += step, e += (int64_t)step * kGatedChunk, ++round) {
+        xr = xn, gr = gn, edge = edge_n;
         if (GATED) zr = zn;
-        if (c_round + step < chunks) {
-            fetch<Tin>(xn, p.x, e + step * kGatedChunk, w);
-            fetch<Tin>(gn, p.g, e + step * kGatedChunk, w);
-            if (GATED) fetch<Tin>(zn, p.z, e + step * kGatedChunk, w);
+        if (c0 + step < chunks) {
+            const int64_t en = e + (int64_t)step * kGatedChunk;
+            edge_n = at_edge(w, c + step, chunks);
+            get<Tin>(xn, p.x, en, w, edge_n);
+            get<Tin>(gn, p.g, en, w, edge_n);
+            if (GATED) get<Tin>(zn, p.z, en, w, edge_n);
         }
-        float x[kE], g[kE], a[kE], b[kE];
-        xr.to_f(x);
-        gr.to_f(g);
-        steps<DECAY>(x, g, nbias, e, w, a, b);
+        float a[kE], b[kE];
+        steps<DECAY>(xr, gr, nbias, a, b);
+        if (edge) mask_steps(e, w, a, b);
         float P = a[0], H = b[0];
 #pragma unroll
         for (int j = 1; j < kE; ++j) {
             H = fmaf(a[j], H, b[j]);
             P *= a[j];
         }
-        scan_up(P, H, lane);
-        const float P31 = __shfl_sync(kFull, P, 31), H31 = __shfl_sync(kFull, H, 31);
-        float Pe = __shfl_up_sync(kFull, P, 1), He = __shfl_up_sync(kFull, H, 1);
-        if (lane == 0) Pe = 1.f, He = 0.f;
-        float in;  // the state entering the warp's chunk
-        if (TEAM) {
-            in = team_round<true>(team, buf, ctas, rank, P31, H31, h);
-        } else {
-            in = h;
-            h = fmaf(P31, h, H31);
-        }
-        if (c < chunks) {
-            if (p.ck && lane == 0) p.ck[r * p.maxch + c] = in;
-            if (p.y) {
-                float hv = fmaf(Pe, in, He);
-                float out[kE], z[kE];
-                if (GATED) zr.to_f(z);
+        scan_up(P, H);
+        float in = h;  // the state entering the warp's chunk
+        if (TEAM) in = team_round<true>(team, round, ctas, rank, P, H, h, alive);
+        const float after = fmaf(P, in, H);  // ... and leaving the lane's steps
+        float hv = __shfl_up_sync(kFull, after, 1);
+        if (lane == 0) hv = in;
+        if (!TEAM) h = __shfl_sync(kFull, after, 31);
+        if (TEAM && c >= chunks) continue;
+        if (p.ck && lane == 0) p.ck[r * p.maxch + c] = in;
+        if (p.y) {
+            float out[kE];
 #pragma unroll
-                for (int j = 0; j < kE; ++j) {
-                    hv = fmaf(a[j], hv, b[j]);
-                    out[j] = GATED ? hv * silu(z[j]) : hv;
+            for (int j = 0; j < kE; ++j) out[j] = hv = fmaf(a[j], hv, b[j]);
+            if (GATED) {
+#pragma unroll
+                for (int i = 0; i < kE / 2; ++i) {
+                    const f2 z = zr.pair(i);
+                    const f2 zs = mul2(z, sigmoid2(mul2(z, twice(-kLog2e))));
+                    unpack2(mul2(pack2(out[2 * i], out[2 * i + 1]), zs), out[2 * i], out[2 * i + 1]);
                 }
-                put<Tout>(p.y, e, w, out);
             }
+            set<Tout>(p.y, e, w, edge, out);
         }
     }
     if (p.last && lane == 0 && (!TEAM || (warp == 0 && rank == 0))) p.last[r] = h;
+    if (TEAM && ctas > 1) cluster_sync();  // what the peers hand over has a place until the end
 }
 
 struct RParams {
@@ -278,50 +319,50 @@ __global__ void __launch_bounds__(TEAM ? 32 * kTeamWarps : 32 * kWarps) gated_bw
     const int ctas = TEAM ? (int)cluster_ctas() : 1, rank = TEAM ? (int)cluster_rank() : 0;
     const int64_t r = TEAM ? blockIdx.x / ctas : (int64_t)blockIdx.x * kWarps + warp;
     if (!TEAM && r >= p.rows) return;
-    if (TEAM && ctas > 1) cluster_sync();  // every CTA's shared memory exists
+    if (TEAM && ctas > 1) team_begin(team);
     const Row w = row_of(r, p.rows, p.L);
-    const int64_t chunks = (w.vectors + 31) / 32;
-    const int64_t step = TEAM ? (int64_t)ctas * (blockDim.x >> 5) : 1;
+    const int chunks = (int)((w.vectors + 31) / 32);
+    const int step = TEAM ? ctas * (int)(blockDim.x >> 5) : 1;
     const float nbias = p.bias ? -kLog2e * __ldg(p.bias + r % p.dim) : 0.f;
     float ec = q.dlast ? __ldg(q.dlast + r) : 0.f, bsum = 0.f;
-    int64_t c_round = (chunks - 1) / step * step;
-    int64_t c = c_round + (TEAM ? (int64_t)rank * (blockDim.x >> 5) + warp : 0);
-    int64_t e = w.base + c * kGatedChunk + lane * kE;
+    int c0 = (chunks - 1) / step * step;
+    int c = c0 + (TEAM ? rank * (int)(blockDim.x >> 5) + warp : 0);
+    int64_t e = w.base + (int64_t)c * kGatedChunk + lane * kE;
+    const float* ck = p.ck + r * p.maxch;
     Raw8<T> xr, gr, yr, zr, xn, gn, yn, zn;
-    float kn = c < chunks ? __ldg(p.ck + r * p.maxch + c) : 0.f;
-    fetch<T>(xn, p.x, e, w);
-    fetch<T>(gn, p.g, e, w);
-    fetch<T>(yn, q.dy, e, w);
-    if (GATED) fetch<T>(zn, p.z, e, w);
-    int buf = 0;
-    for (; c_round >= 0; c_round -= step, c -= step, e -= step * kGatedChunk, buf ^= 1) {
-        xr = xn, gr = gn, yr = yn;
+    bool alive = true, edge, edge_n = at_edge(w, c, chunks);
+    float kn = c < chunks ? __ldg(ck + c) : 0.f;
+    get<T>(xn, p.x, e, w, edge_n);
+    get<T>(gn, p.g, e, w, edge_n);
+    get<T>(yn, q.dy, e, w, edge_n);
+    if (GATED) get<T>(zn, p.z, e, w, edge_n);
+    for (int round = 0; c0 >= 0; c0 -= step, c -= step, e -= (int64_t)step * kGatedChunk, ++round) {
+        xr = xn, gr = gn, yr = yn, edge = edge_n;
         if (GATED) zr = zn;
-        const float entering = kn;
-        if (c_round > 0) {
-            const int64_t en = e - step * kGatedChunk;
-            kn = __ldg(p.ck + r * p.maxch + c - step);
-            fetch<T>(xn, p.x, en, w);
-            fetch<T>(gn, p.g, en, w);
-            fetch<T>(yn, q.dy, en, w);
-            if (GATED) fetch<T>(zn, p.z, en, w);
+        const float entering = kn;  // the state entering the chunk
+        if (c0 > 0) {
+            const int64_t en = e - (int64_t)step * kGatedChunk;
+            edge_n = at_edge(w, c - step, chunks);
+            kn = __ldg(ck + c - step);
+            get<T>(xn, p.x, en, w, edge_n);
+            get<T>(gn, p.g, en, w, edge_n);
+            get<T>(yn, q.dy, en, w, edge_n);
+            if (GATED) get<T>(zn, p.z, en, w, edge_n);
         }
-        float x[kE], g[kE], gy[kE], a[kE], b[kE], z[kE];
-        xr.to_f(x);
-        gr.to_f(g);
-        yr.to_f(gy);
-        steps<DECAY>(x, g, nbias, e, w, a, b);
-        float dz[kE];  // dy times the derivative of silu(z), to be multiplied by the state
-        if (GATED) {
-            zr.to_f(z);
+        float a[kE], b[kE], gy[kE], dz[kE];
+        steps<DECAY>(xr, gr, nbias, a, b);
+        if (edge) mask_steps(e, w, a, b);
 #pragma unroll
-            for (int j = 0; j < kE; ++j) {
-                const float sg = sigmoid_of(z[j] * -kLog2e);
-                dz[j] = gy[j] * (sg * fmaf(z[j], 1.f - sg, 1.f));
-                gy[j] *= z[j] * sg;
+        for (int i = 0; i < kE / 2; ++i) {
+            f2 g = yr.pair(i);
+            if (GATED) {  // dz: dy times the derivative of silu(z), to be multiplied by the state
+                const f2 z = zr.pair(i), s = sigmoid2(mul2(z, twice(-kLog2e)));
+                const f2 ds = mul2(s, fma2(z, sub2(twice(1.f), s), twice(1.f)));
+                unpack2(mul2(g, ds), dz[2 * i], dz[2 * i + 1]);
+                g = mul2(g, mul2(z, s));
             }
+            unpack2(g, gy[2 * i], gy[2 * i + 1]);
         }
-        const bool edge = e < w.lo || e + kE > w.hi;
         if (edge) {
 #pragma unroll
             for (int j = 0; j < kE; ++j)
@@ -334,52 +375,51 @@ __global__ void __launch_bounds__(TEAM ? 32 * kTeamWarps : 32 * kWarps) gated_bw
             P *= a[j];
         }
         float Pd = P;
-        scan_down(Pd, E, lane);
-        const float P0 = __shfl_sync(kFull, Pd, 0), E0 = __shfl_sync(kFull, E, 0);
-        float in;  // the adjoint entering the chunk from its right
-        if (TEAM) {
-            in = team_round<false>(team, buf, ctas, rank, P0, E0, ec);
-            if (c >= chunks) continue;
-        } else {
-            in = ec;
-            ec = fmaf(P0, ec, E0);
-        }
+        scan_down(Pd, E);
+        float in = ec;  // the adjoint entering the chunk from its right
+        if (TEAM) in = team_round<false>(team, round, ctas, rank, Pd, E, ec, alive);
+        const float after = fmaf(Pd, in, E);
+        float ev = __shfl_down_sync(kFull, after, 1);
+        if (lane == 31) ev = in;
+        if (!TEAM) ec = __shfl_sync(kFull, after, 0);
+        if (TEAM && c >= chunks) continue;
         float hv[kE];  // the state before each step
         {
             float H = b[0];
 #pragma unroll
             for (int j = 1; j < kE; ++j) H = fmaf(a[j], H, b[j]);
-            scan_up(P, H, lane);
-            float Pe = __shfl_up_sync(kFull, P, 1), He = __shfl_up_sync(kFull, H, 1);
-            if (lane == 0) Pe = 1.f, He = 0.f;
-            hv[0] = fmaf(Pe, entering, He);
+            scan_up(P, H);
+            hv[0] = __shfl_up_sync(kFull, fmaf(P, entering, H), 1);
+            if (lane == 0) hv[0] = entering;
 #pragma unroll
             for (int j = 1; j < kE; ++j) hv[j] = fmaf(a[j - 1], hv[j - 1], b[j - 1]);
         }
         if (GATED) {
 #pragma unroll
             for (int j = 0; j < kE; ++j) dz[j] *= fmaf(a[j], hv[j], b[j]);
-            put<T>(q.dz, e, w, dz);
+            set<T>(q.dz, e, w, edge, dz);
         }
-        float Pe = __shfl_down_sync(kFull, Pd, 1), Ee = __shfl_down_sync(kFull, E, 1);
-        if (lane == 31) Pe = 1.f, Ee = 0.f;
-        float ev = fmaf(Pe, in, Ee);
-        float dx[kE], dg[kE];
+        float dh[kE];
 #pragma unroll
         for (int j = kE - 1; j >= 0; --j) {
-            const float dh = gy[j] + ev;
-            ev = a[j] * dh;
+            dh[j] = gy[j] + ev;
+            ev = a[j] * dh[j];
+        }
+        float dg[kE];
+#pragma unroll
+        for (int i = 0; i < kE / 2; ++i) {
+            const f2 d = pack2(dh[2 * i], dh[2 * i + 1]), hp = pack2(hv[2 * i], hv[2 * i + 1]);
             if (DECAY) {
-                dx[j] = dh;
-                dg[j] = dh * hv[j];
+                unpack2(mul2(d, hp), dg[2 * i], dg[2 * i + 1]);
             } else {
-                const float s = 1.f - a[j];
-                dx[j] = s * dh;
-                dg[j] = dx[j] * (x[j] - hv[j]) * a[j];
+                const f2 av = pack2(a[2 * i], a[2 * i + 1]);
+                const f2 dx = mul2(sub2(twice(1.f), av), d);
+                unpack2(dx, dh[2 * i], dh[2 * i + 1]);
+                unpack2(mul2(mul2(dx, sub2(xr.pair(i), hp)), av), dg[2 * i], dg[2 * i + 1]);
             }
         }
-        put<T>(q.dx, e, w, dx);
-        put<T>(q.dg, e, w, dg);
+        set<T>(q.dx, e, w, edge, dh);
+        set<T>(q.dg, e, w, edge, dg);
         if (!DECAY) {
             if (edge) {
 #pragma unroll
@@ -404,6 +444,7 @@ __global__ void __launch_bounds__(TEAM ? 32 * kTeamWarps : 32 * kWarps) gated_bw
             q.bias_part[r] = bsum;
         }
     }
+    if (TEAM && ctas > 1) cluster_sync();  // what the peers hand over has a place until the end
 }
 
 // dbias[d]: the partial sums of channel d's rows, in a fixed order (a warp per channel).
@@ -441,7 +482,7 @@ __global__ void __launch_bounds__(128) gated_update_kernel(float* state, const T
         if (DECAY) {
             h.v[j] = fmaf(gf, h.v[j], xf);
         } else {
-            const float s = sigmoid_of(fmaf(gf, -kLog2e, biased ? -kLog2e * bv.v[j] : 0.f));
+            const float s = rcp(1.f + ex2(fmaf(gf, -kLog2e, biased ? -kLog2e * bv.v[j] : 0.f)));
             h.v[j] = fmaf(1.f - s, h.v[j], s * xf);
         }
         yv.v[j] = io<T>::from_f(GATED ? h.v[j] * silu(io<T>::to_f(zv.v[j])) : h.v[j]);
@@ -600,6 +641,17 @@ cudaError_t launch_gated_update(const GatedUpdateArgs& a, cudaStream_t s) {
     if (a.dtype == DType::BF16)
         return a.dim % 4 == 0 ? run_update<__nv_bfloat16, 4>(a, s) : run_update<__nv_bfloat16, 1>(a, s);
     return a.dim % 4 == 0 ? run_update<float, 4>(a, s) : run_update<float, 1>(a, s);
+}
+
+cudaError_t read_gated_error(unsigned* out, bool clear, cudaStream_t s) {
+    cudaError_t e = cudaMemcpyFromSymbolAsync(out, g_gated_error, sizeof(unsigned), 0, cudaMemcpyDeviceToHost, s);
+    if (e == cudaSuccess) e = cudaStreamSynchronize(s);
+    if (e == cudaSuccess && clear && *out) {
+        const unsigned zero = 0;
+        e = cudaMemcpyToSymbolAsync(g_gated_error, &zero, sizeof(zero), 0, cudaMemcpyHostToDevice, s);
+        if (e == cudaSuccess) e = cudaStreamSynchronize(s);
+    }
+    return e;
 }
 
 }  // namespace s6

@@ -56,6 +56,9 @@ cudaError_t launch_gated_scan(const GatedArgs& a, cudaStream_t stream);
 // a.ckpt holds the checkpoints already.
 cudaError_t launch_gated_scan_bwd(const GatedArgs& a, const GatedBwdArgs& g, cudaStream_t stream);
 
+// Bit 0 of the recurrence's device error word (a bounded wait gave up), as read_device_error.
+cudaError_t read_gated_error(unsigned* out, bool clear, cudaStream_t stream);
+
 struct GatedUpdateArgs {
     float* state;  // (batch, dim), updated in place
     const void* x;

@@ -21,6 +21,9 @@ template <> struct Raw8<__nv_bfloat16> {
         v = *reinterpret_cast<const uint4*>(p);
     }
     __device__ __forceinline__ void zero() { v = make_uint4(0u, 0u, 0u, 0u); }
+    __device__ __forceinline__ f2 pair(int i) const {
+        return bf16pair(i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w);
+    }
     __device__ __forceinline__ void to_f(float (&o)[kE]) const {
         const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
@@ -37,6 +40,9 @@ template <> struct Raw8<float> {
         hi = *reinterpret_cast<const float4*>(p + 4);
     }
     __device__ __forceinline__ void zero() { lo = hi = make_float4(0.f, 0.f, 0.f, 0.f); }
+    __device__ __forceinline__ f2 pair(int i) const {
+        return i == 0 ? pack2(lo.x, lo.y) : i == 1 ? pack2(lo.z, lo.w) : i == 2 ? pack2(hi.x, hi.y) : pack2(hi.z, hi.w);
+    }
     __device__ __forceinline__ void to_f(float (&o)[kE]) const {
         o[0] = lo.x, o[1] = lo.y, o[2] = lo.z, o[3] = lo.w;
         o[4] = hi.x, o[5] = hi.y, o[6] = hi.z, o[7] = hi.w;
