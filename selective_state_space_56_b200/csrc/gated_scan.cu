@@ -40,8 +40,8 @@ namespace {
 
 static_assert(kE == kGatedLane, "a lane takes one vector");
 constexpr int kWarps = 4;     // per CTA where a warp walks a row by itself
-constexpr int kTeamWarps = 16;  // at most, per CTA where warps walk a row together
-constexpr int kMaxTeam = 8;     // CTAs of a cluster that walk a row together
+constexpr int kTeamWarps = 8;  // at most, per CTA where warps walk a row together
+constexpr int kMaxTeam = 16;    // at most, CTAs of a cluster that walk a row together
 constexpr unsigned kFull = 0xffffffffu;
 __device__ unsigned int g_gated_error = 0;        // a bounded wait gave up
 constexpr long long kLimit = 2000000000LL;  // SM clocks, about a second
@@ -228,7 +228,7 @@ __device__ __forceinline__ float team_round(Team& team, int round, int ctas, int
 // TEAM: the row's chunks go round the warps of the CTA (and of its cluster); otherwise a warp
 // walks its row alone.  p.y may be null: states (checkpoints, last state) only.
 template <typename Tin, typename Tout, bool DECAY, bool GATED, bool TEAM>
-__global__ void __launch_bounds__(TEAM ? 32 * kTeamWarps : 32 * kWarps, TEAM ? 2 : 1) gated_fwd_kernel(const FParams p) {
+__global__ void __launch_bounds__(TEAM ? 32 * kTeamWarps : 32 * kWarps, TEAM ? 4 : 1) gated_fwd_kernel(const FParams p) {
     __shared__ Team team;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int ctas = TEAM ? (int)cluster_ctas() : 1, rank = TEAM ? (int)cluster_rank() : 0;
@@ -515,6 +515,10 @@ cudaError_t launch_rows(void (*alone)(Params), void (*team)(Params), const Param
     if (t.warps * t.ctas == 1) {
         alone<<<(unsigned)((rows + kWarps - 1) / kWarps), 32 * kWarps, 0, s>>>(p);
         return cudaGetLastError();
+    }
+    if (t.ctas > 8) {  // more than every device allows, but within this one's limit of 16
+        const cudaError_t e = cudaFuncSetAttribute(team, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+        if (e != cudaSuccess) return e;
     }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(rows * t.ctas));
