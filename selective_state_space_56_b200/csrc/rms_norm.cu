@@ -20,15 +20,24 @@ namespace {
 constexpr unsigned kFull = 0xffffffffu;
 constexpr int kMaxThreads = 512;
 
-// Sum of one value (or two) over the CTA, the same bits in every thread.
-__device__ __forceinline__ float2 cta_sum2(float2 v, float2* red) {
+// A row belongs to one CTA, or (ALONE: up to 768 columns) to one of the eight warps of a CTA,
+// which then needs no barrier: a thread's place in the row and the row's threads.
+constexpr int kAloneWarps = 8;
+template <bool ALONE>
+__device__ __forceinline__ int place() { return ALONE ? threadIdx.x & 31 : threadIdx.x; }
+template <bool ALONE>
+__device__ __forceinline__ int threads() { return ALONE ? 32 : blockDim.x; }
+
+// Sum of two values over the row's threads, the same bits in every one.
+template <bool ALONE>
+__device__ __forceinline__ float2 row_sum2(float2 v, float2* red) {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
         v.x += __shfl_xor_sync(kFull, v.x, o);
         v.y += __shfl_xor_sync(kFull, v.y, o);
     }
     const int warps = blockDim.x >> 5;
-    if (warps == 1) return v;
+    if (ALONE || warps == 1) return v;
     if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
     __syncthreads();
     float2 t = red[0];
@@ -60,26 +69,28 @@ __device__ __forceinline__ void weights8(const float* w, int64_t c, int64_t dim,
     }
 }
 
-// One CTA per row, V vectors of 8 per thread.  ALIGNED: dim is a multiple of 8.  OUT: the
+// V vectors of 8 per thread.  ALIGNED: dim is a multiple of 8.  OUT: the
 // output's type; FP8 writes e4m3 and a scale per 128 columns (dim is a multiple of 16 then):
 // 16 lanes hold the 128 columns of a group, and its largest magnitude is their shuffled maximum.
-template <typename Tx, typename Tr, typename Tout, int V, bool ALIGNED, bool FP8>
-__global__ void __launch_bounds__(kMaxThreads) norm_kernel(const NParams p) {
+template <typename Tx, typename Tr, typename Tout, int V, bool ALIGNED, bool FP8, bool ALONE>
+__global__ void __launch_bounds__(ALONE ? 32 * kAloneWarps : kMaxThreads) norm_kernel(const NParams p) {
     __shared__ float2 red[kMaxThreads / 32];
-    const Row w = row_of(blockIdx.x, p.rows, p.dim);
+    const int64_t row = ALONE ? (int64_t)blockIdx.x * kAloneWarps + (threadIdx.x >> 5) : blockIdx.x;
+    if (ALONE && row >= p.rows) return;
+    const Row w = row_of(row, p.rows, p.dim);
     float v[V][kE];
     Raw8<Tx> xr[V];
     Raw8<Tr> rr[V];
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-        const int64_t e = w.base + ((int64_t)i * blockDim.x + threadIdx.x) * kE;
+        const int64_t e = w.base + (i * threads<ALONE>() + place<ALONE>()) * kE;
         fetch<Tx>(xr[i], p.x, e, w);
         if (p.res) fetch<Tr>(rr[i], p.res, e, w);
     }
     float ss = 0.f;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-        const int64_t e = w.base + ((int64_t)i * blockDim.x + threadIdx.x) * kE;
+        const int64_t e = w.base + (i * threads<ALONE>() + place<ALONE>()) * kE;
         xr[i].to_f(v[i]);
         if (p.res) {
             float r[kE];
@@ -96,11 +107,11 @@ __global__ void __launch_bounds__(kMaxThreads) norm_kernel(const NParams p) {
 #pragma unroll
         for (int j = 0; j < kE; ++j) ss = fmaf(v[i][j], v[i][j], ss);
     }
-    const float2 t = cta_sum2(make_float2(ss, 0.f), red);
+    const float2 t = row_sum2<ALONE>(make_float2(ss, 0.f), red);
     const float rstd = rsqrtf(t.x / (float)p.dim + p.eps);
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-        const int64_t e = w.base + ((int64_t)i * blockDim.x + threadIdx.x) * kE;
+        const int64_t e = w.base + (i * threads<ALONE>() + place<ALONE>()) * kE;
         const bool in = e < w.hi;
         float o[kE] = {};
         if (in) {
@@ -123,7 +134,7 @@ __global__ void __launch_bounds__(kMaxThreads) norm_kernel(const NParams p) {
                 *reinterpret_cast<uint2*>(static_cast<uint8_t*>(p.out) + e) = to_e4m3(o);
                 const int64_t c = e - w.lo, groups = (p.dim + kGroup - 1) / kGroup;
                 if (c % kGroup == 0)
-                    p.scales[blockIdx.x * groups + c / kGroup] = m / kE4m3Max;
+                    p.scales[row * groups + c / kGroup] = m / kE4m3Max;
             }
         } else if (in) {
             put<Tout>(p.out, e, w, o);
@@ -143,55 +154,83 @@ struct BNParams {
     float eps;
 };
 
-// CTAs walk rows with the grid's stride and keep their share of dweight in registers; the
-// shares are summed by dweight_kernel in a fixed order (no atomics: the same call gives the
-// same bits).  A thread's columns are the same in every row only when rows begin at vector
-// boundaries; otherwise (dim not a multiple of 8) a thread takes single columns.
-template <typename Tx, typename Tr, int V>
-__global__ void __launch_bounds__(kMaxThreads) norm_bwd_kernel(const BNParams p) {
+// CTAs (or warps: ALONE) walk rows with the grid's stride and keep their share of dweight in
+// registers; the shares are summed by dweight_kernel in a fixed order (no atomics: the same call
+// gives the same bits).  A thread's columns are the same in every row only when rows begin at
+// vector boundaries (dim a multiple of 8); others go to norm_bwd_elem_kernel.  The next row's
+// loads are in flight while this one is computed, which the weights make room for by staying in
+// shared memory.
+template <typename Tx, typename Tr, int V, bool ALONE>
+__global__ void __launch_bounds__(ALONE ? 32 * kAloneWarps : kMaxThreads, ALONE ? 2 : 1) norm_bwd_kernel(const BNParams p) {
     __shared__ float2 red[2][kMaxThreads / 32];
-    float dw[V][kE], wt[V][kE];
+    __shared__ alignas(16) float sums[ALONE ? kAloneWarps * V * 32 * kE : 4];
+    extern __shared__ float4 weight4[];
+    const int64_t first = ALONE ? (int64_t)blockIdx.x * kAloneWarps + (threadIdx.x >> 5) : blockIdx.x;
+    const int64_t stride = ALONE ? (int64_t)gridDim.x * kAloneWarps : gridDim.x;
+    const int dim = (int)p.dim;
+    const auto column = [](int i) { return (i * threads<ALONE>() + place<ALONE>()) * kE; };
+    Raw8<Tx> gn[V];
+    Raw8<Tr> sn[V], dn[V];
+    const auto load = [&](int64_t r) {
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-        const int64_t c = ((int64_t)i * blockDim.x + threadIdx.x) * kE;
+        for (int i = 0; i < V; ++i) {
+            const int64_t e = r * dim + column(i);
+            sn[i].zero(), gn[i].zero();
+            if (p.ds) dn[i].zero();
+            if (column(i) < dim) {
+                sn[i].load(static_cast<const Tr*>(p.s) + e);
+                gn[i].load(static_cast<const Tx*>(p.dout) + e);
+                if (p.ds) dn[i].load(static_cast<const Tr*>(p.ds) + e);
+            }
+        }
+    };
+    if (first < p.rows) load(first);
+    for (int c = threadIdx.x; c < dim / 4; c += blockDim.x) weight4[c] = reinterpret_cast<const float4*>(p.w)[c];
+    __syncthreads();
+    float dw[V][kE];
 #pragma unroll
-        for (int j = 0; j < kE; ++j) dw[i][j] = 0.f, wt[i][j] = 0.f;
-        if (c < p.dim) weights8<true>(p.w, c, p.dim, wt[i]);
-    }
+    for (int i = 0; i < V; ++i)
+#pragma unroll
+        for (int j = 0; j < kE; ++j) dw[i][j] = 0.f;
+    const auto weights = [&](int i, float (&o)[kE]) {
+        const float4 a = weight4[column(i) / 4], b = weight4[column(i) / 4 + 1];
+        o[0] = a.x, o[1] = a.y, o[2] = a.z, o[3] = a.w, o[4] = b.x, o[5] = b.y, o[6] = b.z, o[7] = b.w;
+    };
     int flip = 0;
-    for (int64_t r = blockIdx.x; r < p.rows; r += gridDim.x, flip ^= 1) {
-        const Row w = row_of(r, p.rows, p.dim);
+    for (int64_t r = first; r < p.rows; r += stride, flip ^= 1) {
         Raw8<Tx> gr[V];
         Raw8<Tr> sr[V], dr[V];
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-            const int64_t e = w.base + ((int64_t)i * blockDim.x + threadIdx.x) * kE;
-            fetch<Tr>(sr[i], p.s, e, w);
-            fetch<Tx>(gr[i], p.dout, e, w);
-            if (p.ds) fetch<Tr>(dr[i], p.ds, e, w);
+            sr[i] = sn[i], gr[i] = gn[i];
+            if (p.ds) dr[i] = dn[i];
         }
+        if (r + stride < p.rows) load(r + stride);
         float2 sum = make_float2(0.f, 0.f);
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-            float v[kE], g[kE];
+            if (column(i) >= dim) continue;
+            float v[kE], g[kE], wt[kE];
             sr[i].to_f(v);
             gr[i].to_f(g);
+            weights(i, wt);
 #pragma unroll
             for (int j = 0; j < kE; ++j) {
                 sum.x = fmaf(v[j], v[j], sum.x);
-                sum.y = fmaf(g[j] * wt[i][j], v[j], sum.y);
+                sum.y = fmaf(g[j] * wt[j], v[j], sum.y);
             }
         }
-        sum = cta_sum2(sum, red[flip]);
-        const float rstd = rsqrtf(sum.x / (float)p.dim + p.eps);
-        const float k = sum.y / (float)p.dim * rstd * rstd;  // mean(g xhat) rstd
+        sum = row_sum2<ALONE>(sum, red[flip]);
+        const float rstd = rsqrtf(sum.x / (float)dim + p.eps);
+        const float k = sum.y / (float)dim * rstd * rstd;  // mean(g xhat) rstd
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-            const int64_t e = w.base + ((int64_t)i * blockDim.x + threadIdx.x) * kE;
-            if (e >= w.hi) continue;
-            float v[kE], g[kE], d[kE];
+            if (column(i) >= dim) continue;
+            const int64_t e = r * dim + column(i);
+            float v[kE], g[kE], d[kE], wt[kE];
             sr[i].to_f(v);
             gr[i].to_f(g);
+            weights(i, wt);
             if (p.ds) {
                 dr[i].to_f(d);
             } else {
@@ -201,17 +240,28 @@ __global__ void __launch_bounds__(kMaxThreads) norm_bwd_kernel(const BNParams p)
 #pragma unroll
             for (int j = 0; j < kE; ++j) {
                 dw[i][j] = fmaf(g[j], v[j] * rstd, dw[i][j]);
-                d[j] = fmaf(rstd, fmaf(-k, v[j], g[j] * wt[i][j]), d[j]);
+                d[j] = fmaf(rstd, fmaf(-k, v[j], g[j] * wt[j]), d[j]);
             }
-            put<Tx>(p.dx, e, w, d);
-            if (p.dres) put<Tr>(p.dres, e, w, d);
+            store_all(static_cast<Tx*>(p.dx) + e, d);
+            if (p.dres) store_all(static_cast<Tr*>(p.dres) + e, d);
         }
     }
+    float* part = p.part + (int64_t)blockIdx.x * dim;
+    if (ALONE) {  // the warps' shares, in order
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-        const int64_t c = ((int64_t)i * blockDim.x + threadIdx.x) * kE;
-        if (c < p.dim) store_all(p.part + (int64_t)blockIdx.x * p.dim + c, dw[i]);
+        for (int i = 0; i < V; ++i) store_all(sums + (threadIdx.x >> 5) * V * 32 * kE + column(i), dw[i]);
+        __syncthreads();
+        for (int c = threadIdx.x; c < dim; c += 32 * kAloneWarps) {
+            float t = sums[c];
+#pragma unroll
+            for (int w = 1; w < kAloneWarps; ++w) t += sums[w * V * 32 * kE + c];
+            part[c] = t;
+        }
+        return;
     }
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+        if (column(i) < dim) store_all(part + column(i), dw[i]);
 }
 
 // The same for any dim: a thread takes columns threadIdx.x + i blockDim.x, and dweight's share
@@ -231,7 +281,7 @@ __global__ void __launch_bounds__(kMaxThreads) norm_bwd_elem_kernel(const BNPara
             sum.x = fmaf(v, v, sum.x);
             sum.y = fmaf(g, v, sum.y);
         }
-        sum = cta_sum2(sum, red[flip]);
+        sum = row_sum2<false>(sum, red[flip]);
         const float rstd = rsqrtf(sum.x / (float)p.dim + p.eps);
         const float k = sum.y / (float)p.dim * rstd * rstd;
         for (int64_t c = threadIdx.x; c < p.dim; c += blockDim.x) {
@@ -254,7 +304,8 @@ __global__ void __launch_bounds__(256) dweight_kernel(const float* part, float* 
     const int64_t c = (int64_t)blockIdx.x * 8 + cx;
     float v = 0.f;
     if (c < dim)
-        for (int64_t r = ry; r < blocks; r += 32) v += part[r * dim + c];
+#pragma unroll 8
+        for (int64_t r = ry; r < blocks; r += 32) v += __ldg(part + r * dim + c);
     red[ry][cx] = v;
     __syncthreads();
     if (ry == 0 && c < dim) {
@@ -459,11 +510,20 @@ cudaError_t norm_v(const NParams& p, cudaStream_t s) {
     // a row's vectors: one more where it may begin inside a vector
     const int64_t vectors = ALIGNED ? p.dim / kE : p.dim / kE + 2;
     const unsigned grid = (unsigned)p.rows;
-    if (vectors <= 2 * kMaxThreads)
-        norm_kernel<Tx, Tr, Tout, 2, ALIGNED, FP8><<<grid, threads_for(vectors, 2), 0, s>>>(p);
+    const unsigned alone = (unsigned)((p.rows + kAloneWarps - 1) / kAloneWarps);
+    // a warp per row while it is full (64 vectors) but no longer than three vectors a lane: (16001,
+    // 768) bf16 FIXME
+    if (vectors <= 32)
+        norm_kernel<Tx, Tr, Tout, 1, ALIGNED, FP8, true><<<alone, 32 * kAloneWarps, 0, s>>>(p);
+    else if (vectors <= 64)
+        norm_kernel<Tx, Tr, Tout, 2, ALIGNED, FP8, true><<<alone, 32 * kAloneWarps, 0, s>>>(p);
+    else if (vectors <= 96)
+        norm_kernel<Tx, Tr, Tout, 3, ALIGNED, FP8, true><<<alone, 32 * kAloneWarps, 0, s>>>(p);
+    else if (vectors <= 2 * kMaxThreads)
+        norm_kernel<Tx, Tr, Tout, 2, ALIGNED, FP8, false><<<grid, threads_for(vectors, 2), 0, s>>>(p);
     else {
         constexpr int V = ALIGNED ? 4 : 5;
-        norm_kernel<Tx, Tr, Tout, V, ALIGNED, FP8><<<grid, threads_for(vectors, V), 0, s>>>(p);
+        norm_kernel<Tx, Tr, Tout, V, ALIGNED, FP8, false><<<grid, threads_for(vectors, V), 0, s>>>(p);
     }
     return cudaGetLastError();
 }
@@ -481,12 +541,25 @@ template <typename Tx, typename Tr>
 cudaError_t norm_bwd_t(const BNParams& p, cudaStream_t s) {
     const unsigned grid = (unsigned)norm_bwd_blocks(p.rows, p.dim);
     const int64_t vectors = p.dim / kE;
+    const size_t weights = (size_t)p.dim * 4;
     if (p.dim % kE != 0)
         norm_bwd_elem_kernel<Tx, Tr><<<grid, 256, 0, s>>>(p);
+    else if (vectors <= 32)
+        norm_bwd_kernel<Tx, Tr, 1, true><<<grid, 32 * kAloneWarps, weights, s>>>(p);
+    else if (vectors <= 64)
+        norm_bwd_kernel<Tx, Tr, 2, true><<<grid, 32 * kAloneWarps, weights, s>>>(p);
+    else if (vectors <= 96)
+        norm_bwd_kernel<Tx, Tr, 3, true><<<grid, 32 * kAloneWarps, weights, s>>>(p);
+    else if (vectors <= kMaxThreads)
+        norm_bwd_kernel<Tx, Tr, 1, false><<<grid, threads_for(vectors, 1), weights, s>>>(p);
     else if (vectors <= 2 * kMaxThreads)
-        norm_bwd_kernel<Tx, Tr, 2><<<grid, threads_for(vectors, 2), 0, s>>>(p);
-    else
-        norm_bwd_kernel<Tx, Tr, 4><<<grid, threads_for(vectors, 4), 0, s>>>(p);
+        norm_bwd_kernel<Tx, Tr, 2, false><<<grid, threads_for(vectors, 2), weights, s>>>(p);
+    else {
+        const cudaError_t e = cudaFuncSetAttribute(norm_bwd_kernel<Tx, Tr, 4, false>,
+                                                   cudaFuncAttributeMaxDynamicSharedMemorySize, kNormMaxDim * 4);
+        if (e != cudaSuccess) return e;
+        norm_bwd_kernel<Tx, Tr, 4, false><<<grid, threads_for(vectors, 4), weights, s>>>(p);
+    }
     return cudaGetLastError();
 }
 
@@ -504,6 +577,8 @@ void quantize_cm(const QuantArgs& a, dim3 grid, cudaStream_t s) {
 }  // namespace
 
 int64_t norm_bwd_blocks(int64_t rows, int64_t dim) {
+    if (dim % kE == 0 && dim <= 96 * kE)  // a warp per row
+        return std::max<int64_t>(1, std::min<int64_t>((rows + kAloneWarps - 1) / kAloneWarps, 148 * 2));
     return std::max<int64_t>(1, std::min<int64_t>(rows, 148 * (dim <= 1024 ? 8 : dim <= 4096 ? 4 : 2)));
 }
 
