@@ -28,7 +28,7 @@
 // of a CTA, or of a cluster of CTAs, side by side: each takes one of the next chunks, the
 // chunks' compositions are scanned over the warps (shared memory) and over the CTAs
 // (distributed shared memory), and every array is still read once.  (Cutting rows into segments
-// that are first composed and then walked reads x and gate twice: 126 us against FIXME us for
+// that are first composed and then walked reads x and gate twice: 126 us against 73 for
 // (1, 60, 524287) fp32.)
 #include <algorithm>
 

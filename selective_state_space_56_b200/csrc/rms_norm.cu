@@ -117,8 +117,9 @@ __global__ void __launch_bounds__(ALONE ? 32 * kAloneWarps : kMaxThreads) norm_k
         if (in) {
             float wt[kE];
             weights8<ALIGNED>(p.w, e - w.lo, p.dim, wt);
+            // e4m3: rstd goes into the scale alone, since it cancels in out / scale
 #pragma unroll
-            for (int j = 0; j < kE; ++j) o[j] = v[i][j] * rstd * wt[j];
+            for (int j = 0; j < kE; ++j) o[j] = FP8 ? v[i][j] * wt[j] : v[i][j] * rstd * wt[j];
         }
         if (FP8) {
             float m = 0.f;
@@ -126,15 +127,15 @@ __global__ void __launch_bounds__(ALONE ? 32 * kAloneWarps : kMaxThreads) norm_k
             for (int j = 0; j < kE; ++j) m = fmaxf(m, fabsf(o[j]));
 #pragma unroll
             for (int s = 8; s > 0; s >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, s));
-            m = fmaxf(m, kAmaxFloor);
             if (in) {
-                const float inv = kE4m3Max / m;
+                const float top = m * rstd;  // the group's largest output
+                const float inv = top >= kAmaxFloor ? kE4m3Max / m : rstd * (kE4m3Max / kAmaxFloor);
 #pragma unroll
                 for (int j = 0; j < kE; ++j) o[j] *= inv;
                 *reinterpret_cast<uint2*>(static_cast<uint8_t*>(p.out) + e) = to_e4m3(o);
                 const int64_t c = e - w.lo, groups = (p.dim + kGroup - 1) / kGroup;
                 if (c % kGroup == 0)
-                    p.scales[row * groups + c / kGroup] = m / kE4m3Max;
+                    p.scales[row * groups + c / kGroup] = fmaxf(top, kAmaxFloor) / kE4m3Max;
             }
         } else if (in) {
             put<Tout>(p.out, e, w, o);
@@ -303,6 +304,7 @@ __global__ void __launch_bounds__(256) dweight_kernel(const float* part, float* 
     const int cx = threadIdx.x & 7, ry = threadIdx.x >> 3;
     const int64_t c = (int64_t)blockIdx.x * 8 + cx;
     float v = 0.f;
+    cudaGridDependencySynchronize();  // launched early: wait for the shares
     if (c < dim)
 #pragma unroll 8
         for (int64_t r = ry; r < blocks; r += 32) v += __ldg(part + r * dim + c);
@@ -511,8 +513,8 @@ cudaError_t norm_v(const NParams& p, cudaStream_t s) {
     const int64_t vectors = ALIGNED ? p.dim / kE : p.dim / kE + 2;
     const unsigned grid = (unsigned)p.rows;
     const unsigned alone = (unsigned)((p.rows + kAloneWarps - 1) / kAloneWarps);
-    // a warp per row while it is full (64 vectors) but no longer than three vectors a lane: (16001,
-    // 768) bf16 FIXME
+    // A warp per row up to three vectors a lane, a CTA per row beyond: the training step (16001,
+    // 768) bf16 takes 49.5 us with warps, 56.6 with CTAs of 64 threads.
     if (vectors <= 32)
         norm_kernel<Tx, Tr, Tout, 1, ALIGNED, FP8, true><<<alone, 32 * kAloneWarps, 0, s>>>(p);
     else if (vectors <= 64)
@@ -604,9 +606,19 @@ cudaError_t launch_rms_norm_bwd(const NormBwdArgs& a, cudaStream_t s) {
         e = a.res_dtype == DType::BF16 ? norm_bwd_t<float, __nv_bfloat16>(p, s)
                                        : norm_bwd_t<float, float>(p, s);
     if (e != cudaSuccess) return e;
-    dweight_kernel<<<(unsigned)((a.dim + 7) / 8), 256, 0, s>>>(a.part, a.dweight,
-                                                              norm_bwd_blocks(a.rows, a.dim), a.dim);
-    return cudaGetLastError();
+    // Launched while the backward's last CTAs run (it waits for them before it reads): the training step
+    // (16001, 768) bf16 43.0 -> 41.1 us.
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)((a.dim + 7) / 8));
+    cfg.blockDim = dim3(256);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, dweight_kernel, (const float*)a.part, a.dweight,
+                              norm_bwd_blocks(a.rows, a.dim), a.dim);
 }
 
 cudaError_t launch_fp8_quantize(const QuantArgs& a, cudaStream_t s) {
