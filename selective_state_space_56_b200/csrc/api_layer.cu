@@ -219,11 +219,11 @@ int mamba_add_rms_norm_bwd(const void* dout, const void* residual_out, const flo
 
 int mamba_fp8_quantize(const void* x, void* q, float* scales, int64_t batch, int64_t dim,
                        int64_t seqlen, int channel_major, mamba_dtype dtype, void* stream) {
-    if (batch * seqlen != 0 && (!x || !q || !scales)) return MAMBA_ERR_NULL;
     if (!dtype_ok(dtype)) return MAMBA_ERR_DTYPE;
-    if (batch < 0 || seqlen < 0 || dim < 16 || dim % 16 != 0 || !fits(batch, dim, seqlen) ||
-        !fits(batch, dim + kGroup, seqlen) || batch * seqlen * (dim + kGroup) / 2048 >= kMaxBlocks)
+    if (dim < 16 || dim % 16 != 0 || !fits(batch, dim, seqlen) || !fits(batch, dim + kGroup, seqlen) ||
+        batch * seqlen * (dim + kGroup) / 2048 >= kMaxBlocks)
         return MAMBA_ERR_DIMS;
+    if (batch * seqlen != 0 && (!x || !q || !scales)) return MAMBA_ERR_NULL;
     if (channel_major && (batch > 65535 || dim / kGroup >= 65535)) return MAMBA_ERR_DIMS;
     if (!all_aligned({x, q, scales})) return MAMBA_ERR_ALIGN;
     s6::QuantArgs a{x, q, scales, batch, dim, seqlen, channel_major ? 1 : 0, to_dtype(dtype)};

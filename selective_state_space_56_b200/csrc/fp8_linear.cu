@@ -77,6 +77,9 @@ __device__ __forceinline__ void tma_load_2d(void* dst, const CUtensorMap* map, i
 
 // ---- tcgen05 ---------------------------------------------------------------------------
 
+// An allocation waits until the SM has the columns.  The waits end: the token kernel frees its
+// columns before it waits for other CTAs, and the prefill kernel, whose CTAs hold theirs while they
+// work with their pair, leaves no shared memory on its SMs for any CTA of these kernels.
 __device__ __forceinline__ void tmem_alloc(uint32_t* slot, uint32_t cols) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(slot)),
                  "r"(cols)
@@ -841,6 +844,7 @@ cudaError_t run_token(const LinearArgs& a, const LParams& p, cudaStream_t s) {
     if (!encode_rows(&mx, a.xq, a.k, a.tokens, BN) || !encode_rows(&mw, a.wq, a.k, a.n, kBM))
         return cudaErrorInvalidValue;
     const int64_t tn = (a.n + kBM - 1) / kBM, tt = (a.tokens + BN - 1) / BN;
+    if (tn > 65535 || tt > 65535) return run_prefill<Tout>(a, p, s);  // beyond a grid's y and z
     const int pieces = token_pieces(tn * tt, p.kb);
     const int blocks = (p.kb + pieces - 1) / pieces;
     constexpr uint32_t kStage = token_stage_bytes<BN>();
