@@ -570,6 +570,8 @@ def selective_scan_fold(h_ends, delta_sums, A, h0=None, return_delta_sum=False):
 # ---- The gated linear recurrence --------------------------------------------------------
 
 
+_F32 = torch.float32
+
 # The calls below stand in a decode step's critical path, where a call's host time (about 4 us
 # of it the launch) is longer than its kernel's: they check with as few tensor attribute reads as
 # will do, and go through _check only to say what is wrong.
@@ -631,14 +633,16 @@ def _new(like, shape, dtype):
 
 # The raw handle of a device's current stream: torch.cuda.current_stream builds a Stream object
 # around it (2.2 us against 0.1).
+_calls = {}
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
 def _run(name, dev, *args):
     """One library call on device dev's current stream; raises MambaError for a non-zero status."""
-    fn = getattr(_lib or load_library(), name)
-    if dev == torch.cuda.current_device():
+    fn = _calls.get(name) or _calls.setdefault(name, getattr(load_library(), name))
+    if dev == _current_device():
         rc = fn(*args, _raw_stream(dev))
     else:
         with torch.cuda.device(dev):
@@ -722,16 +726,30 @@ def gated_state_update(state, x, gate, gate_bias=None, z=None, given_decay=False
     x, gate, z: (batch, dim).  Returns y (batch, dim)."""
     dev = _cuda_device(state, "state", "gated_state_update", (2,))
     b, d = shape = state.shape
-    f32 = torch.float32
-    if not isinstance(x, torch.Tensor):
-        raise TypeError("x must be a torch.Tensor")
-    dt = x.dtype
-    code = _dtype(dt, "input")
-    xp = _is(x, "x", dev, shape, dt)
-    y, yp = _output(y, "y", x, dev, shape, dt)
-    _run("mamba_gated_state_update", dev, _is(state, "state", dev, shape, f32), xp, _is(gate, "gate", dev, shape, dt), _maybe(gate_bias, "gate_bias", dev, (d,), f32),
-         _maybe(z, "z", dev, shape, dt), yp, b, d, code,
-         MAMBA_FLAG_GIVEN_DECAY if given_decay else 0)
+    try:
+        dt = x.dtype
+        code = _DTYPES[dt]
+        plain = (x.get_device() == dev and x.shape == shape and x.is_contiguous() and state.dtype is _F32
+                 and gate.get_device() == dev and gate.dtype is dt and gate.shape == shape
+                 and gate.is_contiguous())
+    except (AttributeError, KeyError):
+        plain = False
+    if not plain:
+        if not isinstance(x, torch.Tensor):
+            raise TypeError("x must be a torch.Tensor")
+        dt = x.dtype
+        code = _dtype(dt, "input")
+        for t, name, want in ((state, "state", _F32), (x, "x", dt), (gate, "gate", dt)):
+            _is(t, name, dev, shape, want)
+    bias = None if gate_bias is None else _is(gate_bias, "gate_bias", dev, (d,), _F32)
+    zp = None if z is None else _is(z, "z", dev, shape, dt)
+    if y is None:
+        y = torch.empty_like(x)
+        yp = y.data_ptr()
+    else:
+        yp = _is(y, "y", dev, shape, dt)
+    _run("mamba_gated_state_update", dev, state.data_ptr(), x.data_ptr(), gate.data_ptr(), bias, zp, yp, b,
+         d, code, MAMBA_FLAG_GIVEN_DECAY if given_decay else 0)
     return y
 
 
