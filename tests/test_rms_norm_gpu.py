@@ -97,6 +97,36 @@ def test_add_rms_norm_backward_many_rows(cuda_ok, shape):
     assert all(torch.equal(g[k], again[k]) for k in g)
 
 
+def test_norm_and_quantize_in_graphs_and_streams(cuda_ok):
+    """Captured training steps, replayed on two streams side by side with workspaces of their
+    own, equal the eager calls (dweight's sum starts early there too)."""
+    probs = [problem(3000, 768, "bf16", "bf16", seed=1), problem(700, 2560, "bf16", "fp32", seed=2)]
+
+    def step(p):
+        out, v = ops.add_rms_norm_fwd(p["x"], p["weight"], p["residual"])
+        q, s, _ = ops.add_rms_norm_fp8(p["x"], p["weight"], p["residual"])
+        g = ops.add_rms_norm_bwd(p["dout"], v, p["weight"], p["dres"])
+        return [out, v, q.view(torch.uint8), s, *g.values(), *[t.view(torch.uint8) for t in ops.fp8_quantize(out)]]
+
+    eager = [step(p) for p in probs]
+    graphs, outs = [], []
+    for p in probs:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append(step(p))
+        graphs.append(g)
+    streams = [torch.cuda.Stream() for _ in graphs]
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for g, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                g.replay()
+    torch.cuda.synchronize()
+    for e, o in zip(eager, outs):
+        assert all(torch.equal(a, b) for a, b in zip(e, o))
+    del graphs
+
+
 def test_rms_norm_gradient_against_differences(cuda_ok):
     p = problem(3, 40, "fp32", "fp32", seed=2)
     g = ops.add_rms_norm_bwd(p["dout"], p["residual"], p["weight"], p["dres"])
