@@ -689,8 +689,8 @@ def gated_scan_fwd(x, gate, gate_bias=None, z=None, initial_state=None, given_de
     ck, ck_bytes = _buffer(checkpoints, "checkpoints", dev)
     _run("mamba_gated_scan_fwd", dev, x.data_ptr(), _is(gate, "gate", dev, shape, in_dt),
          _maybe(gate_bias, "gate_bias", dev, (d,), f32), _maybe(z, "z", dev, shape, in_dt),
-         _maybe(initial_state, "initial_state", dev, (b, d), f32), yp, lp, ck, ck_bytes, GatedDims(b, d, L), in_code,
-         out_code, MAMBA_FLAG_GIVEN_DECAY if given_decay else 0)
+         _maybe(initial_state, "initial_state", dev, (b, d), f32), yp, lp, ck, ck_bytes,
+         GatedDims(b, d, L), in_code, out_code, MAMBA_FLAG_GIVEN_DECAY if given_decay else 0)
     return (y, last_state) if return_last_state else y
 
 
@@ -705,7 +705,8 @@ def gated_scan_bwd(x, gate, dy, gate_bias=None, z=None, initial_state=None, dlas
     b, d, L = shape = x.shape
     dt, f32 = x.dtype, torch.float32
     code = _dtype(dt, "input")
-    g = dict(dx=_new(x, shape, dt), dgate=_new(x, shape, dt), dz=None if z is None else _new(x, shape, dt),
+    g = dict(dx=_new(x, shape, dt), dgate=_new(x, shape, dt),
+             dz=None if z is None else _new(x, shape, dt),
              dgate_bias=None if gate_bias is None or given_decay else _new(x, (d,), f32),
              dinitial_state=_new(x, (b, d), f32))
     ck, ck_bytes = _buffer(checkpoints, "checkpoints", dev)
@@ -715,8 +716,8 @@ def gated_scan_bwd(x, gate, dy, gate_bias=None, z=None, initial_state=None, dlas
     _run("mamba_gated_scan_bwd", dev, x.data_ptr(), _is(gate, "gate", dev, shape, dt),
          _maybe(gate_bias, "gate_bias", dev, (d,), f32), _maybe(z, "z", dev, shape, dt),
          _maybe(initial_state, "initial_state", dev, (b, d), f32), _is(dy, "dy", dev, shape, dt),
-         _maybe(dlast_state, "dlast_state", dev, (b, d), f32), g["dx"].data_ptr(), g["dgate"].data_ptr(),
-         _addr(g["dz"]), _addr(g["dgate_bias"]), g["dinitial_state"].data_ptr(), ck, ck_bytes, dims,
+         _maybe(dlast_state, "dlast_state", dev, (b, d), f32), g["dx"].data_ptr(),
+         g["dgate"].data_ptr(), _addr(g["dz"]), _addr(g["dgate_bias"]), g["dinitial_state"].data_ptr(), ck, ck_bytes, dims,
          code, ws, ws_bytes, MAMBA_FLAG_GIVEN_DECAY if given_decay else 0)
     return g
 
@@ -729,8 +730,8 @@ def gated_state_update(state, x, gate, gate_bias=None, z=None, given_decay=False
     try:
         dt = x.dtype
         code = _DTYPES[dt]
-        plain = (x.get_device() == dev and x.shape == shape and x.is_contiguous() and state.dtype is _F32
-                 and gate.get_device() == dev and gate.dtype is dt and gate.shape == shape
+        plain = (x.get_device() == dev and x.shape == shape and x.is_contiguous()
+                 and state.dtype is _F32 and gate.get_device() == dev and gate.dtype is dt and gate.shape == shape
                  and gate.is_contiguous())
     except (AttributeError, KeyError):
         plain = False
@@ -748,8 +749,8 @@ def gated_state_update(state, x, gate, gate_bias=None, z=None, given_decay=False
         yp = y.data_ptr()
     else:
         yp = _is(y, "y", dev, shape, dt)
-    _run("mamba_gated_state_update", dev, state.data_ptr(), x.data_ptr(), gate.data_ptr(), bias, zp, yp, b,
-         d, code, MAMBA_FLAG_GIVEN_DECAY if given_decay else 0)
+    _run("mamba_gated_state_update", dev, state.data_ptr(), x.data_ptr(), gate.data_ptr(), bias, zp,
+         yp, b, d, code, MAMBA_FLAG_GIVEN_DECAY if given_decay else 0)
     return y
 
 
@@ -776,8 +777,8 @@ def _norm_inputs(x, weight, residual, residual_out, where):
         rp = _is(residual, "residual", dev, shape, rt)
     op = None
     if residual is not None or residual_out is not None:
-        residual_out, op = _output(residual_out, "residual_out", x if residual is None else residual, dev,
-                                   shape, rt)
+        like = x if residual is None else residual
+        residual_out, op = _output(residual_out, "residual_out", like, dev, shape, rt)
     rows = shape[0] if len(shape) == 2 else shape[0] * shape[1]
     return (dev, d, rows, code, rcode, x.data_ptr(), rp,
             _is(weight, "weight", dev, (d,), torch.float32), op, residual_out)
@@ -834,7 +835,8 @@ def add_rms_norm_bwd(dout, residual_out, weight, dresidual_out=None, eps=1e-5, w
     rows = shape[0] if len(shape) == 2 else shape[0] * shape[1]
     need = (_lib or load_library()).mamba_add_rms_norm_bwd_workspace_size(rows, d)
     workspace, ws, ws_bytes = _workspace(workspace, need, dout, dev)
-    _run("mamba_add_rms_norm_bwd", dev, dout.data_ptr(), _is(residual_out, "residual_out", dev, shape, rt), _is(weight, "weight", dev, (d,), f32),
+    _run("mamba_add_rms_norm_bwd", dev, dout.data_ptr(),
+         _is(residual_out, "residual_out", dev, shape, rt), _is(weight, "weight", dev, (d,), f32),
          _maybe(dresidual_out, "dresidual_out", dev, shape, rt), eps, dx.data_ptr(), _addr(dres),
          dw.data_ptr(), rows, d, code, rcode, ws, ws_bytes)
     return dict(dx=dx, dresidual=dx if dres is None else dres, dweight=dw)
