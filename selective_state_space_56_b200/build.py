@@ -7,6 +7,9 @@ Every .cu under csrc/ is compiled separately (in parallel) with
 ``selective_state_space_56_b200/libmamba_s6.so`` with the CUDA runtime linked
 statically, so the library loads next to any PyTorch build.  Objects and the
 ``-Xptxas -v`` report go to ``_build/`` at the repository root.
+
+``csrc/binding.cpp`` (native argument checks and allocations for the layer operators) is
+compiled with g++ against the interpreter's own PyTorch into ``_native.so`` beside it.
 """
 from __future__ import annotations
 
@@ -17,6 +20,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -25,6 +29,8 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(ROOT, "_build")
 LIB_NAME = "libmamba_s6.so"
 LIB_PATH = os.path.join(PKG, LIB_NAME)
+BINDING = os.path.join(CSRC, "binding.cpp")
+BINDING_PATH = os.path.join(PKG, "_native.so")
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xptxas", "-v",
@@ -55,7 +61,29 @@ def up_to_date() -> bool:
     return all(os.path.getmtime(f) <= t for f in _deps())
 
 
+def _build_binding(force: bool) -> None:
+    header = os.path.join(INCLUDE, "mamba_s6.h")
+    if (not force and os.path.exists(BINDING_PATH)
+            and os.path.getmtime(BINDING_PATH) >= max(map(os.path.getmtime, (BINDING, header)))):
+        return
+    import torch
+    from torch.utils import cpp_extension
+    inc = cpp_extension.include_paths() + [sysconfig.get_paths()["include"], INCLUDE]
+    cuda = os.path.join(os.path.dirname(os.path.dirname(_nvcc())), "include")
+    lib = cpp_extension.library_paths()[0]
+    tmp = BINDING_PATH + ".tmp%d" % os.getpid()
+    cmd = (["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-w",
+            '-DS6_TORCH_VERSION="%s"' % torch.__version__] + ["-I" + d for d in inc + [cuda]] +
+           [BINDING, "-o", tmp, "-L" + lib, "-Wl,-rpath," + lib, "-ltorch_python", "-ltorch",
+            "-ltorch_cpu", "-ltorch_cuda", "-lc10", "-lc10_cuda"])
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError("g++ failed on %s:\n%s" % (BINDING, r.stderr))
+    os.replace(tmp, BINDING_PATH)
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
+    _build_binding(force)
     if not force and up_to_date():
         return LIB_PATH
     nvcc = _nvcc()

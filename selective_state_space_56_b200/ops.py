@@ -10,6 +10,7 @@ no fallback: if the library is missing or the ABI rejects the call, a
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import os
 import threading
 
@@ -41,11 +42,30 @@ class GatedDims(ctypes.Structure):
 
 _lock = threading.Lock()
 _lib = None
+_native = None
+
+
+def _load_native(lib):
+    """The native marshalling of the layer operators' calls, or None where it is not built, or
+    was built against another torch."""
+    path = os.path.join(_HERE, "_native.so")
+    if not os.path.exists(path):
+        return None
+    try:
+        spec = importlib.util.spec_from_file_location("_native", path)
+        mod = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(mod)
+    except ImportError:
+        return None
+    if mod.torch_version != torch.__version__:
+        return None
+    mod.bind({n: ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in mod.names()})
+    return mod
 
 
 def load_library():
     """Load libmamba_s6.so (build it first with ``python -m selective_state_space_56_b200.build``)."""
-    global _lib
+    global _lib, _native
     with _lock:
         if _lib is None:
             if not os.path.exists(LIB_PATH):
@@ -135,6 +155,7 @@ def load_library():
             lib.mamba_diag_throughput.argtypes = [i32, i64, i64, vp, vp]
             lib.mamba_abi_version.restype = i32
             lib.mamba_abi_version.argtypes = []
+            _native = _load_native(lib)
             _lib = lib
     return _lib
 
@@ -570,13 +591,6 @@ def selective_scan_fold(h_ends, delta_sums, A, h0=None, return_delta_sum=False):
 # ---- The gated linear recurrence --------------------------------------------------------
 
 
-_F32 = torch.float32
-
-# The calls below stand in a decode step's critical path, where a call's host time (about 4 us
-# of it the launch) is longer than its kernel's: they check with as few tensor attribute reads as
-# will do, and go through _check only to say what is wrong.
-
-
 def _cuda_device(t, name, where, ndim):
     if not isinstance(t, torch.Tensor) or t.dim() not in ndim:
         raise ValueError("%s must be a tensor of %s dimensions" % (name, " or ".join(map(str, ndim))))
@@ -677,6 +691,12 @@ def gated_scan_fwd(x, gate, gate_bias=None, z=None, initial_state=None, given_de
     dim) fp32 (zero when None).  Returns y (batch, dim, L) [and last_state (batch, dim) fp32].
     checkpoints: a uint8 CUDA tensor of gated_scan_checkpoints_size(...) bytes to record what
     ``gated_scan_bwd`` starts from."""
+    flags = MAMBA_FLAG_GIVEN_DECAY if given_decay else 0
+    if _native is not None and y is None and last_state is None and out_dtype is None:
+        r = _native.gated_scan_fwd(x, gate, gate_bias, z, initial_state, checkpoints, flags,
+                                   bool(return_last_state))
+        if r is not None:
+            return r if return_last_state else r[0]
     dev = _cuda_device(x, "x", "gated_scan_fwd", (3,))
     b, d, L = shape = x.shape
     in_dt, f32 = x.dtype, torch.float32
@@ -690,7 +710,7 @@ def gated_scan_fwd(x, gate, gate_bias=None, z=None, initial_state=None, given_de
     _run("mamba_gated_scan_fwd", dev, x.data_ptr(), _is(gate, "gate", dev, shape, in_dt),
          _maybe(gate_bias, "gate_bias", dev, (d,), f32), _maybe(z, "z", dev, shape, in_dt),
          _maybe(initial_state, "initial_state", dev, (b, d), f32), yp, lp, ck, ck_bytes,
-         GatedDims(b, d, L), in_code, out_code, MAMBA_FLAG_GIVEN_DECAY if given_decay else 0)
+         GatedDims(b, d, L), in_code, out_code, flags)
     return (y, last_state) if return_last_state else y
 
 
@@ -701,6 +721,12 @@ def gated_scan_bwd(x, gate, dy, gate_bias=None, z=None, initial_state=None, dlas
     without z), dgate_bias (dim) fp32 (None without a bias or with given_decay),
     dinitial_state (batch, dim) fp32.  checkpoints: the buffer the forward filled for the same
     inputs; without it the backward makes one more pass over x and gate."""
+    flags = MAMBA_FLAG_GIVEN_DECAY if given_decay else 0
+    if _native is not None and workspace is None:
+        r = _native.gated_scan_bwd(x, gate, dy, gate_bias, z, initial_state, dlast_state, checkpoints,
+                                   flags)
+        if r is not None:
+            return dict(dx=r[0], dgate=r[1], dz=r[2], dgate_bias=r[3], dinitial_state=r[4])
     dev = _cuda_device(x, "x", "gated_scan_bwd", (3,))
     b, d, L = shape = x.shape
     dt, f32 = x.dtype, torch.float32
@@ -717,40 +743,31 @@ def gated_scan_bwd(x, gate, dy, gate_bias=None, z=None, initial_state=None, dlas
          _maybe(gate_bias, "gate_bias", dev, (d,), f32), _maybe(z, "z", dev, shape, dt),
          _maybe(initial_state, "initial_state", dev, (b, d), f32), _is(dy, "dy", dev, shape, dt),
          _maybe(dlast_state, "dlast_state", dev, (b, d), f32), g["dx"].data_ptr(),
-         g["dgate"].data_ptr(), _addr(g["dz"]), _addr(g["dgate_bias"]), g["dinitial_state"].data_ptr(), ck, ck_bytes, dims,
-         code, ws, ws_bytes, MAMBA_FLAG_GIVEN_DECAY if given_decay else 0)
+         g["dgate"].data_ptr(), _addr(g["dz"]), _addr(g["dgate_bias"]), g["dinitial_state"].data_ptr(), ck, ck_bytes,
+         dims, code, ws, ws_bytes, flags)
     return g
 
 
 def gated_state_update(state, x, gate, gate_bias=None, z=None, given_decay=False, y=None):
     """One decode token of the gated recurrence, in place on ``state`` (batch, dim) fp32;
     x, gate, z: (batch, dim).  Returns y (batch, dim)."""
+    flags = MAMBA_FLAG_GIVEN_DECAY if given_decay else 0
+    if _native is not None and y is None:
+        r = _native.gated_state_update(state, x, gate, gate_bias, z, flags)
+        if r is not None:
+            return r
     dev = _cuda_device(state, "state", "gated_state_update", (2,))
     b, d = shape = state.shape
-    try:
-        dt = x.dtype
-        code = _DTYPES[dt]
-        plain = (x.get_device() == dev and x.shape == shape and x.is_contiguous()
-                 and state.dtype is _F32 and gate.get_device() == dev and gate.dtype is dt and gate.shape == shape
-                 and gate.is_contiguous())
-    except (AttributeError, KeyError):
-        plain = False
-    if not plain:
-        if not isinstance(x, torch.Tensor):
-            raise TypeError("x must be a torch.Tensor")
-        dt = x.dtype
-        code = _dtype(dt, "input")
-        for t, name, want in ((state, "state", _F32), (x, "x", dt), (gate, "gate", dt)):
-            _is(t, name, dev, shape, want)
-    bias = None if gate_bias is None else _is(gate_bias, "gate_bias", dev, (d,), _F32)
-    zp = None if z is None else _is(z, "z", dev, shape, dt)
-    if y is None:
-        y = torch.empty_like(x)
-        yp = y.data_ptr()
-    else:
-        yp = _is(y, "y", dev, shape, dt)
-    _run("mamba_gated_state_update", dev, state.data_ptr(), x.data_ptr(), gate.data_ptr(), bias, zp,
-         yp, b, d, code, MAMBA_FLAG_GIVEN_DECAY if given_decay else 0)
+    f32 = torch.float32
+    if not isinstance(x, torch.Tensor):
+        raise TypeError("x must be a torch.Tensor")
+    dt = x.dtype
+    code = _dtype(dt, "input")
+    xp = _is(x, "x", dev, shape, dt)
+    y, yp = _output(y, "y", x, dev, shape, dt)
+    _run("mamba_gated_state_update", dev, _is(state, "state", dev, shape, f32), xp,
+         _is(gate, "gate", dev, shape, dt), _maybe(gate_bias, "gate_bias", dev, (d,), f32),
+         _maybe(z, "z", dev, shape, dt), yp, b, d, code, flags)
     return y
 
 
@@ -789,6 +806,10 @@ def add_rms_norm_fwd(x, weight, residual=None, eps=1e-5, out_dtype=None, out=Non
     """v = residual + x (in the residual's dtype); out = v / sqrt(mean v^2 + eps) * weight.
     x, residual: (..., dim) of 2 or 3 dimensions, weight: (dim) fp32.  Returns (out, v);
     without a residual v is x."""
+    if _native is not None and out_dtype is None and out is None and residual_out is None:
+        r = _native.add_rms_norm_fwd(x, weight, residual, eps)
+        if r is not None:
+            return r if residual is not None else (r[0], x)
     dev, d, rows, code, rcode, xp, rp, wp, op, residual_out = _norm_inputs(
         x, weight, residual, residual_out, "add_rms_norm_fwd")
     out_dt = x.dtype if out_dtype is None else out_dtype
@@ -801,6 +822,10 @@ def add_rms_norm_fwd(x, weight, residual=None, eps=1e-5, out_dtype=None, out=Non
 def add_rms_norm_fp8(x, weight, residual=None, eps=1e-5, q=None, scales=None, residual_out=None):
     """``add_rms_norm_fwd`` with the output in e4m3: returns (q (..., dim) float8_e4m3fn,
     scales (..., ceil(dim / 128)) fp32, v), out = q * scale.  dim a multiple of 16."""
+    if _native is not None and q is None and scales is None and residual_out is None:
+        r = _native.add_rms_norm_fp8(x, weight, residual, eps)
+        if r is not None:
+            return r if residual is not None else (r[0], r[1], x)
     dev, d, rows, code, rcode, xp, rp, wp, op, residual_out = _norm_inputs(
         x, weight, residual, residual_out, "add_rms_norm_fp8")
     q, scales, qp, sp = _fp8_outputs(x, q, scales, x.shape[:-1], d, dev)
@@ -821,6 +846,10 @@ def add_rms_norm_bwd(dout, residual_out, weight, dresidual_out=None, eps=1e-5, w
     dtype; dresidual_out: the gradient arriving at v from elsewhere, in its dtype.  Returns a
     dict: dx (dout's dtype), dresidual (v's dtype; the same tensor where the dtypes agree),
     dweight (dim) fp32."""
+    if _native is not None and workspace is None:
+        r = _native.add_rms_norm_bwd(dout, residual_out, weight, dresidual_out, eps)
+        if r is not None:
+            return dict(dx=r[0], dresidual=r[0] if r[1] is None else r[1], dweight=r[2])
     dev = _cuda_device(dout, "dout", "add_rms_norm_bwd", (2, 3))
     shape, dt, f32 = dout.shape, dout.dtype, torch.float32
     d = shape[-1]
@@ -850,6 +879,10 @@ def fp8_quantize(x, channel_major=False, q=None, scales=None):
     (batch, dim, L) with channel_major (the layout of the scans' y).  Returns (q (tokens, dim)
     float8_e4m3fn, scales (tokens, ceil(dim / 128)) fp32), tokens = batch * L in the latter
     case.  dim a multiple of 16."""
+    if _native is not None and q is None and scales is None:
+        r = _native.fp8_quantize(x, bool(channel_major))
+        if r is not None:
+            return r
     dev = _cuda_device(x, "x", "fp8_quantize", (3,) if channel_major else (2,))
     code = _dtype(x.dtype, "input")
     b, d, L = x.shape if channel_major else (1, x.shape[1], x.shape[0])
@@ -877,8 +910,14 @@ def fp8_linear(xq, x_scales, wq, w_scales, out_dtype=torch.bfloat16, channel_maj
     """The projection x w^T of operands in e4m3 (``fp8_quantize`` / ``add_rms_norm_fp8`` and
     ``fp8_quantize_weight``): xq (tokens, k), wq (n, k).  Returns (tokens, n), or with
     channel_major_seqlen = L the layout of the conv's and the scans' inputs, (tokens / L, n, L)."""
-    dev = _cuda_device(xq, "xq", "fp8_linear", (2,))
     code = _dtype(out_dtype, "output")
+    if _native is not None and out is None:
+        L = channel_major_seqlen
+        if L is None or (type(L) is int and L > 0):
+            r = _native.fp8_linear(xq, x_scales, wq, w_scales, code, L or 0)
+            if r is not None:
+                return r
+    dev = _cuda_device(xq, "xq", "fp8_linear", (2,))
     t, k = xq.shape
     n = wq.shape[0] if isinstance(wq, torch.Tensor) and wq.dim() == 2 else -1
     f8, f32, kb = torch.float8_e4m3fn, torch.float32, (k + 127) // 128
