@@ -565,12 +565,23 @@ token_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUt
     const int pieces = (int)gridDim.x, piece = (int)cluster_rank();
     const int k0 = (int)((int64_t)p.kb * piece / pieces), k1 = (int)((int64_t)p.kb * (piece + 1) / pieces);
     const int64_t n0 = (int64_t)blockIdx.y * kBM, t0 = (int64_t)blockIdx.z * BN;
-    if (threadIdx.x == 128) {
+    const CUtensorMap *map_x = &mx, *map_w = &mw;
+    const auto load = [=](int k, int s) {
+        uint8_t* st = ring + (size_t)s * kStage;
+        uint64_t* full = &bars.full[s];
+        mbar_arrive_expect_tx(full, kStage);
+        tma_load_2d(st, map_w, k * kBK, (int)n0, full);
+        tma_load_2d(st + kBM * kBK, map_x, k * kBK, (int)t0, full);
+    };
+    const int ahead = min(stages, k1 - k0);  // blocks that find their stage empty
+    if (warp == 4 && elect_one()) {
         for (int i = 0; i < stages; ++i) mbar_init(&bars.full[i], 1), mbar_init(&bars.empty[i], 1);
         for (int i = 0; i < kTurns; ++i) mbar_init(&bars.done[i], 1), mbar_init(&bars.free[i], 4);
         mbar_init(&bars.drain, 1);
         bars.ctl.abort = 0;
         fence_barrier_init();
+        // the first loads are on their way while the others set up
+        for (int i = 0; i < ahead; ++i) load(k0 + i, i);
     }
     if (warp == 5) tmem_alloc(&bars.tmem, kCols);
     tc_fence_before();
@@ -580,17 +591,14 @@ token_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUt
     if (warp == 4) {
         if (elect_one()) {
             int s = 0;
-            uint32_t phase = 0;
-            for (int k = k0; k < k1; ++k) {
+            uint32_t phase = 1;
+            for (int k = k0 + ahead; k < k1; ++k) {  // ahead == stages here: stage 0 comes next
                 if (!wait_or_abort(&bars.empty[s], phase ^ 1u, &bars.ctl)) {
-                    for (int j = 0; j < min(stages, k - k0); ++j)  // copies in flight
+                    for (int j = 0; j < stages; ++j)  // copies in flight
                         mbar_wait_bounded(&bars.full[j], j < s ? phase : phase ^ 1u, kLimit / 8);
                     break;
                 }
-                uint8_t* st = ring + (size_t)s * kStage;
-                mbar_arrive_expect_tx(&bars.full[s], kStage);
-                tma_load_2d(st, &mw, k * kBK, (int)n0, &bars.full[s]);
-                tma_load_2d(st + kBM * kBK, &mx, k * kBK, (int)t0, &bars.full[s]);
+                load(k, s);
                 if (++s == stages) s = 0, phase ^= 1u;
             }
         }
