@@ -452,6 +452,7 @@ __global__ void gated_bias_kernel(const float* part, float* dbias, int64_t batch
                                   int64_t parts) {
     const int lane = threadIdx.x & 31;
     const int64_t d = (int64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
+    cudaGridDependencySynchronize();  // launched early: wait for the rows' sums
     if (d >= dim) return;
     float v = 0.f;
     for (int64_t i = lane; i < batch * parts; i += 32)
@@ -628,16 +629,22 @@ cudaError_t launch_gated_scan_bwd(const GatedArgs& a, const GatedBwdArgs& g, cud
     q.dg = g.dgate;
     q.dz = g.dz;
     q.dh0 = g.dh0;
-    q.bias_part = g.dbias ? g.bias_part : nullptr;
-    cudaError_t e = a.in_dtype == DType::BF16 ? run_bwd_t<__nv_bfloat16>(q, a.given_decay != 0, s)
-                                              : run_bwd_t<float>(q, a.given_decay != 0, s);
-    if (e == cudaSuccess && g.dbias) {
-        gated_bias_kernel<<<(unsigned)((a.dim + 3) / 4), 128, 0, s>>>(g.bias_part, g.dbias,
-                                                                     a.rows / a.dim, a.dim,
-                                                                     gated_team(a.rows, a.L, true).ctas);
-        e = cudaGetLastError();
-    }
-    return e;
+    const int64_t batch = a.rows / a.dim, parts = gated_team(a.rows, a.L, true).ctas;
+    const bool whole = batch * parts == 1;  // a row's sum is the channel's
+    q.bias_part = !g.dbias ? nullptr : whole ? g.dbias : g.bias_part;
+    const cudaError_t e = a.in_dtype == DType::BF16 ? run_bwd_t<__nv_bfloat16>(q, a.given_decay != 0, s)
+                                                    : run_bwd_t<float>(q, a.given_decay != 0, s);
+    if (e != cudaSuccess || !g.dbias || whole) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)((a.dim + 3) / 4));
+    cfg.blockDim = dim3(128);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, gated_bias_kernel, (const float*)g.bias_part, g.dbias, batch, a.dim, parts);
 }
 
 cudaError_t launch_gated_update(const GatedUpdateArgs& a, cudaStream_t s) {
