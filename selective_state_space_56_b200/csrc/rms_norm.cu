@@ -63,6 +63,9 @@ __device__ __forceinline__ void weights8(const float* w, int64_t c, int64_t dim,
         Raw8<float> r;
         r.load(w + c);
         r.to_f(o);
+    } else if (c >= 0 && c + kE <= dim) {
+#pragma unroll
+        for (int j = 0; j < kE; ++j) o[j] = __ldg(w + c + j);
     } else {
 #pragma unroll
         for (int j = 0; j < kE; ++j) o[j] = (c + j >= 0 && c + j < dim) ? __ldg(w + c + j) : 0.f;
@@ -98,7 +101,7 @@ __global__ void __launch_bounds__(ALONE ? 32 * kAloneWarps : kMaxThreads) norm_k
 #pragma unroll
             for (int j = 0; j < kE; ++j) v[i][j] = io<Tr>::to_f(io<Tr>::from_f(v[i][j] + r[j]));
         }
-        if (!ALIGNED) {
+        if (!ALIGNED && (e < w.lo || e + kE > w.hi)) {
 #pragma unroll
             for (int j = 0; j < kE; ++j)
                 if (e + j < w.lo || e + j >= w.hi) v[i][j] = 0.f;
@@ -265,36 +268,66 @@ __global__ void __launch_bounds__(ALONE ? 32 * kAloneWarps : kMaxThreads, ALONE 
         if (column(i) < dim) store_all(part + column(i), dw[i]);
 }
 
-// The same for any dim: a thread takes columns threadIdx.x + i blockDim.x, and dweight's share
-// goes through its row of `part` in memory.
-template <typename Tx, typename Tr>
+// The same for any dim: a thread takes C single columns, threadIdx.x + i blockDim.x, of every
+// row, so that its share of dweight stays in registers there too; the next row's values are on
+// their way while this one is computed.  (16384, 1023) bf16: 122 us with two passes over a row
+// and shares in memory, 57 so.
+template <typename Tx, typename Tr, int C>
 __global__ void __launch_bounds__(kMaxThreads) norm_bwd_elem_kernel(const BNParams p) {
     __shared__ float2 red[2][kMaxThreads / 32];
-    float* part = p.part + (int64_t)blockIdx.x * p.dim;
-    const Tx* dout = static_cast<const Tx*>(p.dout);
-    const Tr *st = static_cast<const Tr*>(p.s), *ds = static_cast<const Tr*>(p.ds);
+    const int dim = (int)p.dim;
+    const auto column = [](int i) { return (int)(threadIdx.x + i * blockDim.x); };
+    Tr sn[C], dn[C];
+    Tx gn[C];
+    const auto load = [&](int64_t r) {
+        const int64_t at = r * dim;
+#pragma unroll
+        for (int i = 0; i < C; ++i) {
+            const int c = column(i);
+            sn[i] = dn[i] = io<Tr>::from_f(0.f), gn[i] = io<Tx>::from_f(0.f);
+            if (c < dim) {
+                sn[i] = static_cast<const Tr*>(p.s)[at + c];
+                gn[i] = static_cast<const Tx*>(p.dout)[at + c];
+                if (p.ds) dn[i] = static_cast<const Tr*>(p.ds)[at + c];
+            }
+        }
+    };
+    load(blockIdx.x);  // no more CTAs than rows
+    float wt[C], dw[C];
+#pragma unroll
+    for (int i = 0; i < C; ++i) {
+        wt[i] = column(i) < dim ? __ldg(p.w + column(i)) : 0.f;
+        dw[i] = 0.f;
+    }
     int flip = 0;
     for (int64_t r = blockIdx.x; r < p.rows; r += gridDim.x, flip ^= 1) {
+        float v[C], g[C], d[C];
+#pragma unroll
+        for (int i = 0; i < C; ++i) v[i] = io<Tr>::to_f(sn[i]), g[i] = io<Tx>::to_f(gn[i]), d[i] = io<Tr>::to_f(dn[i]);
+        if (r + gridDim.x < p.rows) load(r + gridDim.x);
         float2 sum = make_float2(0.f, 0.f);
-        for (int64_t c = threadIdx.x; c < p.dim; c += blockDim.x) {
-            const float v = io<Tr>::to_f(st[r * p.dim + c]);
-            const float g = io<Tx>::to_f(dout[r * p.dim + c]) * __ldg(p.w + c);
-            sum.x = fmaf(v, v, sum.x);
-            sum.y = fmaf(g, v, sum.y);
+#pragma unroll
+        for (int i = 0; i < C; ++i) {
+            sum.x = fmaf(v[i], v[i], sum.x);
+            sum.y = fmaf(g[i] * wt[i], v[i], sum.y);
         }
         sum = row_sum2<false>(sum, red[flip]);
-        const float rstd = rsqrtf(sum.x / (float)p.dim + p.eps);
-        const float k = sum.y / (float)p.dim * rstd * rstd;
-        for (int64_t c = threadIdx.x; c < p.dim; c += blockDim.x) {
-            const float v = io<Tr>::to_f(st[r * p.dim + c]), g = io<Tx>::to_f(dout[r * p.dim + c]);
-            const float d = fmaf(rstd, fmaf(-k, v, g * __ldg(p.w + c)),
-                                 ds ? io<Tr>::to_f(ds[r * p.dim + c]) : 0.f);
-            const float dw = g * (v * rstd);
-            part[c] = r == blockIdx.x ? dw : part[c] + dw;
-            static_cast<Tx*>(p.dx)[r * p.dim + c] = io<Tx>::from_f(d);
-            if (p.dres) static_cast<Tr*>(p.dres)[r * p.dim + c] = io<Tr>::from_f(d);
+        const float rstd = rsqrtf(sum.x / (float)dim + p.eps);
+        const float k = sum.y / (float)dim * rstd * rstd;
+        const int64_t at = r * dim;
+#pragma unroll
+        for (int i = 0; i < C; ++i) {
+            dw[i] = fmaf(g[i], v[i] * rstd, dw[i]);
+            d[i] = fmaf(rstd, fmaf(-k, v[i], g[i] * wt[i]), d[i]);
+            if (column(i) < dim) {
+                static_cast<Tx*>(p.dx)[at + column(i)] = io<Tx>::from_f(d[i]);
+                if (p.dres) static_cast<Tr*>(p.dres)[at + column(i)] = io<Tr>::from_f(d[i]);
+            }
         }
     }
+#pragma unroll
+    for (int i = 0; i < C; ++i)
+        if (column(i) < dim) p.part[(int64_t)blockIdx.x * dim + column(i)] = dw[i];
 }
 
 // Columns' sums of part (blocks, dim): 8 columns per CTA, 32 rows side by side.
@@ -544,9 +577,12 @@ cudaError_t norm_bwd_t(const BNParams& p, cudaStream_t s) {
     const unsigned grid = (unsigned)norm_bwd_blocks(p.rows, p.dim);
     const int64_t vectors = p.dim / kE;
     const size_t weights = (size_t)p.dim * 4;
-    if (p.dim % kE != 0)
-        norm_bwd_elem_kernel<Tx, Tr><<<grid, 256, 0, s>>>(p);
-    else if (vectors <= 32)
+    if (p.dim % kE != 0) {
+        const auto threads = [&](int C) { return (unsigned)(((p.dim + C - 1) / C + 31) / 32 * 32); };
+        if (p.dim <= 4 * kMaxThreads) norm_bwd_elem_kernel<Tx, Tr, 4><<<grid, threads(4), 0, s>>>(p);
+        else if (p.dim <= 8 * kMaxThreads) norm_bwd_elem_kernel<Tx, Tr, 8><<<grid, threads(8), 0, s>>>(p);
+        else norm_bwd_elem_kernel<Tx, Tr, 32><<<grid, threads(32), 0, s>>>(p);
+    } else if (vectors <= 32)
         norm_bwd_kernel<Tx, Tr, 1, true><<<grid, 32 * kAloneWarps, weights, s>>>(p);
     else if (vectors <= 64)
         norm_bwd_kernel<Tx, Tr, 2, true><<<grid, 32 * kAloneWarps, weights, s>>>(p);
@@ -581,7 +617,7 @@ void quantize_cm(const QuantArgs& a, dim3 grid, cudaStream_t s) {
 int64_t norm_bwd_blocks(int64_t rows, int64_t dim) {
     if (dim % kE == 0 && dim <= 96 * kE)  // a warp per row
         return std::max<int64_t>(1, std::min<int64_t>((rows + kAloneWarps - 1) / kAloneWarps, 148 * 2));
-    return std::max<int64_t>(1, std::min<int64_t>(rows, 148 * (dim <= 1024 ? 8 : dim <= 4096 ? 4 : 2)));
+    return std::max<int64_t>(1, std::min<int64_t>(rows, 148 * (dim <= 4096 ? 4 : 2)));
 }
 
 cudaError_t launch_rms_norm(const NormArgs& a, cudaStream_t s) {
