@@ -316,32 +316,48 @@ __device__ __forceinline__ void store_tile(const LParams& p, const CUtensorMap* 
     const int64_t t = t0 + lane;
     Tout* out = static_cast<Tout*>(p.out);
     if (p.seqlen == 0) {
-        if (p.out_tma) {
 #pragma unroll
-            for (int r = 0; r < kPCols / kRound; ++r) {
-                uint8_t* st = stage + (r & 1) * 4096;
-                if (lane == 0) tma_store_wait_read<1>();  // the round before the last has left its piece
-                __syncwarp();
+        for (int r = 0; r < kPCols / kRound; ++r) {
+            uint8_t* st = stage + (r & 1) * 4096;
+            if (p.out_tma && lane == 0) tma_store_wait_read<1>();  // the round before the last has left its piece
+            __syncwarp();
 #pragma unroll
-                for (int c = 0; c < 8; ++c) {  // 128-byte swizzle: piece c of row i at c ^ (i % 8)
-                    alignas(16) Tout v[kPer];
+            for (int c = 0; c < 8; ++c) {  // 128-byte swizzle: piece c of row i at c ^ (i % 8)
+                alignas(16) Tout v[kPer];
 #pragma unroll
-                    for (int j = 0; j < kPer; ++j) v[j] = io<Tout>::from_f(acc[r * kRound + c * kPer + j]);
-                    *reinterpret_cast<uint4*>(st + lane * 128 + ((c ^ (lane & 7)) * 16)) =
-                        *reinterpret_cast<uint4*>(v);
-                }
+                for (int j = 0; j < kPer; ++j) v[j] = io<Tout>::from_f(acc[r * kRound + c * kPer + j]);
+                *reinterpret_cast<uint4*>(st + lane * 128 + ((c ^ (lane & 7)) * 16)) = *reinterpret_cast<uint4*>(v);
+            }
+            const int64_t col0 = n0 + r * kRound;
+            if (p.out_tma) {
                 fence_proxy_async();
                 __syncwarp();
                 if (lane == 0) {
-                    tma_store_2d(mo, st, (int)n0 + r * kRound, (int)t0);
+                    tma_store_2d(mo, st, (int)col0, (int)t0);
                     tma_store_commit();
                 }
+                continue;
             }
-        } else if (t < p.tokens) {
-            Tout* o = out + t * p.n + n0;
+            // Rows that begin anywhere: the lanes run along a row, 4 bytes each.  (A lane storing its own
+            // token's row touches 32 lines a store: 166 us against 53 for 4096 tokens, 2560 -> 3001.)
+            __syncwarp();
+            const int rows = (int)min((int64_t)32, p.tokens - t0);
+            constexpr int kEach = 4 / sizeof(Tout);
+            const int64_t col = col0 + lane * kEach;
+#pragma unroll 4
+            for (int i = 0; i < rows; ++i) {
+                const uint32_t v = *reinterpret_cast<const uint32_t*>(st + i * 128 + (((lane >> 2) ^ (i & 7)) * 16) +
+                                                                       (lane & 3) * 4);
+                Tout* o = out + (t0 + i) * p.n + col;
+                if (col + kEach <= p.n && (reinterpret_cast<uintptr_t>(o) & 3) == 0) {
+                    *reinterpret_cast<uint32_t*>(o) = v;
+                } else {
+                    const Tout* e = reinterpret_cast<const Tout*>(&v);
 #pragma unroll
-            for (int c = 0; c < kPCols; ++c)
-                if (n0 + c < p.n) o[c] = io<Tout>::from_f(acc[c]);
+                    for (int j = 0; j < kEach; ++j)
+                        if (col + j < p.n) o[j] = e[j];
+                }
+            }
         }
         return;
     }
