@@ -462,34 +462,65 @@ __global__ void gated_bias_kernel(const float* part, float* dbias, int64_t batch
     if (lane == 0) dbias[d] = v;
 }
 
-// One token: h = a h + b in place, a stream over (batch, dim).  V elements per thread.
-template <typename T, bool DECAY, bool GATED, int V>
+// One token: h = a h + b in place, a stream over (batch, dim), four elements per thread.  The
+// bias is read as a vector where rows are whole vectors, else element by element, and the last
+// thread takes the elements behind the last whole vector: (256, 5121) bf16 with z 6.8 -> 4.4 us
+// against one element per thread.
+constexpr int kUpdate = 4;
+template <typename T, bool DECAY, bool GATED>
 __global__ void __launch_bounds__(128) gated_update_kernel(float* state, const T* x, const T* gate,
                                                            const float* bias, const T* z, T* y,
                                                            int64_t n, int64_t dim) {
-    const int64_t i = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) * V;
+    const int64_t i = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) * kUpdate;
     if (i >= n) return;
-    struct alignas(V * sizeof(T)) TV { T v[V]; };
-    struct alignas(V * 4) FV { float v[V]; };
-    const TV xv = *reinterpret_cast<const TV*>(x + i), gv = *reinterpret_cast<const TV*>(gate + i);
-    TV zv, yv;
-    if (GATED) zv = *reinterpret_cast<const TV*>(z + i);
-    FV h = *reinterpret_cast<const FV*>(state + i), bv;
-    const bool biased = !DECAY && bias != nullptr;
-    if (biased) bv = *reinterpret_cast<const FV*>(bias + i % dim);
+    struct alignas(kUpdate * sizeof(T)) TV { T v[kUpdate]; };
+    const int count = (int)min((int64_t)kUpdate, n - i);
+    TV xv, gv, zv, yv;
+    float4 h4 = make_float4(0.f, 0.f, 0.f, 0.f), b4 = h4;
+    float *h = &h4.x, *b = &b4.x;
+    if (count == kUpdate) {
+        xv = *reinterpret_cast<const TV*>(x + i), gv = *reinterpret_cast<const TV*>(gate + i);
+        if (GATED) zv = *reinterpret_cast<const TV*>(z + i);
+        h4 = *reinterpret_cast<const float4*>(state + i);
+    } else {
 #pragma unroll
-    for (int j = 0; j < V; ++j) {
+        for (int j = 0; j < kUpdate; ++j) {
+            const int64_t k = i + min(j, count - 1);
+            xv.v[j] = x[k], gv.v[j] = gate[k], h[j] = state[k];
+            if (GATED) zv.v[j] = z[k];
+        }
+    }
+    if (!DECAY && bias != nullptr) {
+        int64_t d = i % dim;
+        if (dim % kUpdate == 0) {
+            b4 = *reinterpret_cast<const float4*>(bias + d);
+        } else {
+#pragma unroll
+            for (int j = 0; j < kUpdate; ++j) {
+                b[j] = __ldg(bias + d);
+                if (++d == dim) d = 0;
+            }
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < kUpdate; ++j) {
         const float xf = io<T>::to_f(xv.v[j]), gf = io<T>::to_f(gv.v[j]);
         if (DECAY) {
-            h.v[j] = fmaf(gf, h.v[j], xf);
+            h[j] = fmaf(gf, h[j], xf);
         } else {
-            const float s = rcp(1.f + ex2(fmaf(gf, -kLog2e, biased ? -kLog2e * bv.v[j] : 0.f)));
-            h.v[j] = fmaf(1.f - s, h.v[j], s * xf);
+            const float s = rcp(1.f + ex2(fmaf(gf, -kLog2e, -kLog2e * b[j])));
+            h[j] = fmaf(1.f - s, h[j], s * xf);
         }
-        yv.v[j] = io<T>::from_f(GATED ? h.v[j] * silu(io<T>::to_f(zv.v[j])) : h.v[j]);
+        yv.v[j] = io<T>::from_f(GATED ? h[j] * silu(io<T>::to_f(zv.v[j])) : h[j]);
     }
-    *reinterpret_cast<FV*>(state + i) = h;
-    *reinterpret_cast<TV*>(y + i) = yv;
+    if (count == kUpdate) {
+        *reinterpret_cast<float4*>(state + i) = h4;
+        *reinterpret_cast<TV*>(y + i) = yv;
+    } else {
+#pragma unroll
+        for (int j = 0; j < kUpdate; ++j)
+            if (j < count) state[i + j] = h[j], y[i + j] = yv.v[j];
+    }
 }
 
 FParams fparams(const GatedArgs& a) {
@@ -560,20 +591,15 @@ cudaError_t run_bwd_t(const RParams& q, bool decay, cudaStream_t s) {
     return gated ? run_bwd<T, false, true>(q, s) : run_bwd<T, false, false>(q, s);
 }
 
-template <typename T, int V>
+template <typename T>
 cudaError_t run_update(const GatedUpdateArgs& a, cudaStream_t s) {
     const int64_t n = a.batch * a.dim;
-    const unsigned blocks = (unsigned)((n / V + 127) / 128);
-    const T *x = static_cast<const T*>(a.x), *g = static_cast<const T*>(a.gate),
-            *z = static_cast<const T*>(a.z);
+    const unsigned blocks = (unsigned)((n + 128 * kUpdate - 1) / (128 * kUpdate));
+    const T *x = static_cast<const T*>(a.x), *g = static_cast<const T*>(a.gate), *z = static_cast<const T*>(a.z);
     T* y = static_cast<T*>(a.y);
-    if (a.given_decay) {
-        if (z) gated_update_kernel<T, true, true, V><<<blocks, 128, 0, s>>>(a.state, x, g, a.gate_bias, z, y, n, a.dim);
-        else gated_update_kernel<T, true, false, V><<<blocks, 128, 0, s>>>(a.state, x, g, a.gate_bias, z, y, n, a.dim);
-    } else {
-        if (z) gated_update_kernel<T, false, true, V><<<blocks, 128, 0, s>>>(a.state, x, g, a.gate_bias, z, y, n, a.dim);
-        else gated_update_kernel<T, false, false, V><<<blocks, 128, 0, s>>>(a.state, x, g, a.gate_bias, z, y, n, a.dim);
-    }
+    const auto kernel = a.given_decay ? (z ? gated_update_kernel<T, true, true> : gated_update_kernel<T, true, false>)
+                                      : (z ? gated_update_kernel<T, false, true> : gated_update_kernel<T, false, false>);
+    kernel<<<blocks, 128, 0, s>>>(a.state, x, g, a.gate_bias, z, y, n, a.dim);
     return cudaGetLastError();
 }
 
@@ -648,10 +674,7 @@ cudaError_t launch_gated_scan_bwd(const GatedArgs& a, const GatedBwdArgs& g, cud
 }
 
 cudaError_t launch_gated_update(const GatedUpdateArgs& a, cudaStream_t s) {
-    // Vectors of 4 where a row is a whole number of them (the bias is read as a vector too).
-    if (a.dtype == DType::BF16)
-        return a.dim % 4 == 0 ? run_update<__nv_bfloat16, 4>(a, s) : run_update<__nv_bfloat16, 1>(a, s);
-    return a.dim % 4 == 0 ? run_update<float, 4>(a, s) : run_update<float, 1>(a, s);
+    return a.dtype == DType::BF16 ? run_update<__nv_bfloat16>(a, s) : run_update<float>(a, s);
 }
 
 cudaError_t read_gated_error(unsigned* out, bool clear, cudaStream_t s) {

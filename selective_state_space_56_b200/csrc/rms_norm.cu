@@ -352,34 +352,48 @@ __global__ void __launch_bounds__(256) dweight_kernel(const float* part, float* 
 
 // ---- Quantisation --------------------------------------------------------------------
 
-// Row-major: a thread takes 8 values, 16 lanes a group of 128; rows are padded to whole groups
-// in the thread numbering only.
-template <typename T>
+// Row-major: 16 lanes take a group of 128, 8 values each, and kBatch groups one after another
+// whose loads are issued together.  Groups are numbered over rows padded to whole ones; WHOLE
+// (dim a multiple of 128): group g lies at 128 g.  (16384, 2560) bf16: 29.2 us with one
+// group a thread, 21.0 us (6.05 TB/s) with four.
+constexpr int kBatch = 4;
+template <typename T, bool WHOLE>
 __global__ void __launch_bounds__(256) quantize_kernel(const T* x, uint8_t* q, float* scales,
                                                        int64_t rows, int64_t dim) {
-    const int64_t groups = (dim + kGroup - 1) / kGroup;
-    const int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
-    const int64_t gi = i >> 4;  // (row, group)
-    const int64_t r = gi / groups, c = (gi - r * groups) * kGroup + (i & 15) * kE;
-    const bool in = r < rows && c < dim;
-    float v[kE] = {};
-    if (in) {
-        Raw8<T> raw;
-        raw.load(x + r * dim + c);
-        raw.to_f(v);
+    const int64_t groups = (dim + kGroup - 1) / kGroup, all = rows * groups;
+    const int64_t g0 = (int64_t)blockIdx.x * (16 * kBatch) + (threadIdx.x >> 4);
+    const int lane = threadIdx.x & 15;
+    int64_t at[kBatch];
+    Raw8<T> raw[kBatch];
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+        const int64_t g = g0 + i * 16;
+        at[i] = -1;
+        if (WHOLE) {
+            if (g < all) at[i] = g * kGroup + lane * kE;
+        } else {
+            const int64_t r = g / groups, c = (g - r * groups) * kGroup + lane * kE;
+            if (r < rows && c < dim) at[i] = r * dim + c;
+        }
+        raw[i].zero();
+        if (at[i] >= 0) raw[i].load(x + at[i]);
     }
-    float m = 0.f;
 #pragma unroll
-    for (int j = 0; j < kE; ++j) m = fmaxf(m, fabsf(v[j]));
+    for (int i = 0; i < kBatch; ++i) {
+        float v[kE], m = 0.f;
+        raw[i].to_f(v);
 #pragma unroll
-    for (int s = 8; s > 0; s >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, s));
-    m = fmaxf(m, kAmaxFloor);
-    if (!in) return;
-    const float inv = kE4m3Max / m;
+        for (int j = 0; j < kE; ++j) m = fmaxf(m, fabsf(v[j]));
 #pragma unroll
-    for (int j = 0; j < kE; ++j) v[j] *= inv;
-    *reinterpret_cast<uint2*>(q + r * dim + c) = to_e4m3(v);
-    if ((i & 15) == 0) scales[gi] = m / kE4m3Max;
+        for (int s = 8; s > 0; s >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, s));
+        m = fmaxf(m, kAmaxFloor);
+        if (at[i] < 0) continue;
+        const float inv = kE4m3Max / m;
+#pragma unroll
+        for (int j = 0; j < kE; ++j) v[j] *= inv;
+        *reinterpret_cast<uint2*>(q + at[i]) = to_e4m3(v);
+        if (lane == 0) scales[g0 + i * 16] = m / kE4m3Max;
+    }
 }
 
 // Channel-major (batch, dim, L) to token rows (batch * L, dim): a CTA takes 128 channels of 64
@@ -602,6 +616,15 @@ cudaError_t norm_bwd_t(const BNParams& p, cudaStream_t s) {
 }
 
 template <typename T>
+void quantize_rows(const QuantArgs& a, int64_t rows, cudaStream_t s) {
+    const T* x = static_cast<const T*>(a.x);
+    uint8_t* q = static_cast<uint8_t*>(a.q);
+    const unsigned grid = (unsigned)((rows * ((a.dim + kGroup - 1) / kGroup) + 16 * kBatch - 1) / (16 * kBatch));
+    if (a.dim % kGroup == 0) quantize_kernel<T, true><<<grid, 256, 0, s>>>(x, q, a.scales, rows, a.dim);
+    else quantize_kernel<T, false><<<grid, 256, 0, s>>>(x, q, a.scales, rows, a.dim);
+}
+
+template <typename T>
 void quantize_cm(const QuantArgs& a, dim3 grid, cudaStream_t s) {
     const T* x = static_cast<const T*>(a.x);
     uint8_t* q = static_cast<uint8_t*>(a.q);
@@ -661,13 +684,9 @@ cudaError_t launch_fp8_quantize(const QuantArgs& a, cudaStream_t s) {
     const int64_t rows = a.batch * a.seqlen;
     if (rows == 0) return cudaSuccess;
     const int64_t groups = (a.dim + kGroup - 1) / kGroup;
-    uint8_t* q = static_cast<uint8_t*>(a.q);
     if (!a.channel_major) {
-        const unsigned grid = (unsigned)((rows * groups * 16 + 255) / 256);
-        if (a.dtype == DType::BF16)
-            quantize_kernel<<<grid, 256, 0, s>>>(static_cast<const __nv_bfloat16*>(a.x), q, a.scales, rows, a.dim);
-        else
-            quantize_kernel<<<grid, 256, 0, s>>>(static_cast<const float*>(a.x), q, a.scales, rows, a.dim);
+        if (a.dtype == DType::BF16) quantize_rows<__nv_bfloat16>(a, rows, s);
+        else quantize_rows<float>(a, rows, s);
         return cudaGetLastError();
     }
     const dim3 grid((unsigned)((a.seqlen + kTok - 1) / kTok), (unsigned)groups, (unsigned)a.batch);
