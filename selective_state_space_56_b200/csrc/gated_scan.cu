@@ -667,6 +667,8 @@ FParams fparams(const GatedArgs& a) {
     return p;
 }
 
+constexpr int kPlainShared = 46 * 1024;  // a launch's dynamic shared memory without further permission
+
 // Launches `alone` with a warp per row, or `team` with the plan's warps and CTAs per row, and so many
 // bytes of shared memory for each warp's ring.
 template <int ALONE_RING, int TEAM_RING, typename Params>
@@ -675,13 +677,17 @@ cudaError_t launch_rows(void (*alone)(Params), void (*team)(Params), const Param
     cudaError_t e;
     if (t.warps * t.ctas == 1) {
         constexpr int kBytes = kWarps * ALONE_RING;
-        e = cudaFuncSetAttribute(alone, cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes);
-        if (e != cudaSuccess) return e;
+        if (kBytes > kPlainShared) {
+            e = cudaFuncSetAttribute(alone, cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes);
+            if (e != cudaSuccess) return e;
+        }
         alone<<<(unsigned)((rows + kWarps - 1) / kWarps), 32 * kWarps, kBytes, s>>>(p);
         return cudaGetLastError();
     }
-    e = cudaFuncSetAttribute(team, cudaFuncAttributeMaxDynamicSharedMemorySize, kTeamWarps * TEAM_RING);
-    if (e != cudaSuccess) return e;
+    if (kTeamWarps * TEAM_RING > kPlainShared) {
+        e = cudaFuncSetAttribute(team, cudaFuncAttributeMaxDynamicSharedMemorySize, kTeamWarps * TEAM_RING);
+        if (e != cudaSuccess) return e;
+    }
     if (t.ctas > 8) {  // more than every device allows, but within this one's limit of 16
         e = cudaFuncSetAttribute(team, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
         if (e != cudaSuccess) return e;
