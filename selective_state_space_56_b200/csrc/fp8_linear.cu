@@ -14,6 +14,8 @@
 //                    CTAs (cta_group::2): each loads half of either operand, which halves the
 //                    weights' share of the shared-memory traffic that a 128 x 256 tile of one CTA is
 //                    bound by.  A lane is a token, so its scale is one register a block.
+//                    16384 tokens, 2560 -> 10240: 391 us, 2.2 PFLOP/s, the tensor pipe 52% busy;
+//                    bound by the summing warps' reads of tensor memory.
 //   token_kernel     few tokens: bound by the weights' bytes.  128 outputs are the MMA's rows,
 //                    the tokens its columns (16 to 64), and the inputs are cut into pieces over a
 //                    cluster whose CTAs add their sums through distributed shared memory in
@@ -192,8 +194,8 @@ __device__ __forceinline__ void tmem_ld_wait(uint32_t (&r)[32]) {
     asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
     pin32(r);
 }
-// acc += r * scale on 32 columns.  (Packed pairs measured slower, 449 against 420 us for 16384
-// tokens, 2560 -> 10240.)
+// acc += r * scale on 32 columns.  (Packed pairs were 7% slower for 16384 tokens, 2560 ->
+// 10240.)
 __device__ __forceinline__ void add_scaled(float* acc, const uint32_t (&r)[32], float scale) {
 #pragma unroll
     for (int j = 0; j < 32; ++j) acc[j] = fmaf(__uint_as_float(r[j]), scale, acc[j]);
@@ -477,20 +479,26 @@ prefill_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ C
         const uint32_t free0 = peer_addr(&bars.free[0], 0), free1 = peer_addr(&bars.free[1], 0);
         Turn<2> d;
         uint32_t ra[32], rb[32];
+        int64_t t0, n0;  // the warp's first token and output of a tile
+        const float *xs, *ws;
+        float xn, wn;  // the scales of the block to come
+        const auto begin = [&](int tile) {
+            const int tt = tile / p.tiles_n, tn = tile - tt * p.tiles_n;
+            t0 = (int64_t)tt * kPT + rank * kBM + quad * 32;
+            n0 = (int64_t)tn * kPN + part * kPCols;
+            const bool in = t0 + lane < p.tokens && n0 < p.n;
+            xs = p.xs + (in ? t0 + lane : 0) * p.kb;
+            ws = p.ws + (in ? n0 / kGroup : 0) * p.kb;
+            xn = __ldg(xs), wn = __ldg(ws);
+        };
+        if (pair < tiles) begin(pair);
         bool ok = __all_sync(kFull, wait_or_abort(&bars.done[0], 0, &bars.ctl));
         tc_fence_after();
         if (ok) tmem_ld32(base, ra);
         for (int tile = pair; tile < tiles && ok; tile += pairs) {
-            const int tt = tile / p.tiles_n, tn = tile - tt * p.tiles_n;
-            const int64_t t0 = (int64_t)tt * kPT + rank * kBM + quad * 32;  // the warp's first token
-            const int64_t n0 = (int64_t)tn * kPN + part * kPCols;
-            const bool in = t0 + lane < p.tokens && n0 < p.n;
-            const float* xs = p.xs + (in ? t0 + lane : 0) * p.kb;
-            const float* ws = p.ws + (in ? n0 / kGroup : 0) * p.kb;
             float acc[kPCols];
 #pragma unroll
             for (int i = 0; i < kPCols; ++i) acc[i] = 0.f;
-            float xn = __ldg(xs), wn = __ldg(ws);
             for (int k = 0; k < p.kb; ++k) {
                 const float sc = xn * wn;
                 if (k + 1 < p.kb) xn = __ldg(xs + k + 1), wn = __ldg(ws + k + 1);  // used a block later
@@ -521,7 +529,9 @@ prefill_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ C
                 add_scaled(acc + 96, rb, sc);
             }
             if (!ok) break;
-            if (n0 < p.n && t0 < p.tokens) store_tile<Tout>(p, &mo, stage, t0, n0, lane, acc);
+            const int64_t t_done = t0, n_done = n0;
+            if (tile + pairs < tiles) begin(tile + pairs);  // its first scales arrive during the stores
+            if (n_done < p.n && t_done < p.tokens) store_tile<Tout>(p, &mo, stage, t_done, n_done, lane, acc);
         }
         if (lane == 0) tma_store_wait_all();
     }
@@ -839,27 +849,31 @@ int token_pieces(int64_t tiles, int kb) {
     return (int)pieces;
 }
 
-// Columns (tokens) of the token kernel's tiles.
-int token_columns(int64_t tokens) { return tokens <= 16 ? 16 : tokens <= 32 ? 32 : 64; }
-
-// Whether the prefill kernel is the faster one.  Both times are close to straight lines in the
-// input blocks walked one after another, fitted to launches of (64 .. 4096 tokens) x (768 .. 10240
-// outputs) x (1536 .. 5120 inputs), weights in L2:
-//   prefill  7 us + 0.43 us a block and wave of 74 tiles of 256 x 256
-//   token    5 us + 0.80 us a block, longer in proportion once the CTAs exceed two an SM
-// (128 tokens, 2560 -> 10240: 16.4 against 19.8 us; 64 tokens: 15.7 against 11.4; 256 tokens,
-// 5120 -> 2560: 25.2 against 15.4; 1024 tokens: 26.8 against 50).
-bool prefill_is_faster(const LinearArgs& a, int kb) {
+// Which kernel: the token kernel with tiles of 16, 32 or 64 tokens, or (0) the prefill kernel.  Each
+// one's time is close to a straight line in the input blocks that a CTA walks one after another,
+// times the waves of CTAs; fitted to launches of (16 .. 4096 tokens) x (80 .. 10240 outputs) x
+// (1536 .. 10240 inputs), weights in L2:
+//   prefill  7 us + 0.39 us a block        token, 64  7 us + 0.60
+//   token, 32  6 us + 0.40                 token, 16  5 us + 0.28
+// Narrow tiles cut a call into more CTAs, wide ones read the weights fewer times.  Measured, 16, 32, 64
+// and prefill: 32 tokens, 5120 -> 2560: 7.1, 8.2, 9.3, 21.6 us; 64 tokens, 2560 -> 5120: 10.5, 8.9,
+// 10.1, 13.7; 256 tokens, 5120 -> 2560: -, 21.2, 15.4, 22.6; 128 tokens, 2560 -> 10240: -, 23.8, 19.7,
+// 15.1.
+int best_columns(const LinearArgs& a, int kb) {
+    struct Line { int columns; double fixed, block; };
+    constexpr Line kToken[3] = {{16, 5.0, 0.28}, {32, 6.0, 0.40}, {64, 7.0, 0.60}};
     const int64_t sms = multiprocessors();
-    const int64_t big = ((a.tokens + kPT - 1) / kPT) * ((a.n + kPN - 1) / kPN);
-    const int64_t pairs = std::max<int64_t>(1, sms / 2);
-    const double prefill = 7.0 + 0.43 * kb * (double)((big + pairs - 1) / pairs);
-    const int bn = token_columns(a.tokens);
-    const int64_t tiles = ((a.n + kBM - 1) / kBM) * ((a.tokens + bn - 1) / bn);
-    const int pieces = token_pieces(tiles, kb);
-    const double full = 1.1 * (double)(tiles * pieces) / (double)(2 * sms);
-    const double token = 5.0 + 0.8 * ((kb + pieces - 1) / pieces) * std::max(1.0, full);
-    return prefill < token;
+    const auto ceil_div = [](int64_t x, int64_t y) { return (x + y - 1) / y; };
+    int best = 0;
+    double least = 7.0 + 0.39 * kb * (double)ceil_div(ceil_div(a.tokens, kPT) * ceil_div(a.n, kPN),
+                                                      std::max<int64_t>(1, sms / 2));
+    for (const Line& l : kToken) {
+        const int64_t tiles = ceil_div(a.n, kBM) * ceil_div(a.tokens, l.columns);
+        const int pieces = token_pieces(tiles, kb);
+        const double time = l.fixed + l.block * (double)ceil_div(kb, pieces) * (double)ceil_div(tiles * pieces, 2 * sms);
+        if (time < least) least = time, best = l.columns;
+    }
+    return best;
 }
 
 template <int BN, typename Tout>
@@ -910,11 +924,11 @@ cudaError_t run_linear(const LinearArgs& a, cudaStream_t s) {
     p.seqlen = a.seqlen;
     p.kb = (int)((a.k + kBK - 1) / kBK);
     p.tiles_t = p.tiles_n = p.out_tma = 0;
-    if (prefill_is_faster(a, p.kb)) return run_prefill<Tout>(a, p, s);
-    switch (token_columns(a.tokens)) {
+    switch (best_columns(a, p.kb)) {
         case 16: return run_token<16, Tout>(a, p, s);
         case 32: return run_token<32, Tout>(a, p, s);
-        default: return run_token<64, Tout>(a, p, s);
+        case 64: return run_token<64, Tout>(a, p, s);
+        default: return run_prefill<Tout>(a, p, s);
     }
 }
 

@@ -60,6 +60,17 @@ def test_fp8_linear_many_tokens(cuda_ok, shape, out):
     compare(*shape, out=out, seed=1)
 
 
+@pytest.mark.parametrize("shape", [(61, 5120, 2560), (77, 4000, 2576), (59, 10240, 2560), (150, 4999, 2064),
+                                   (231, 2555, 4112), (1001, 130, 1536)], ids=lambda s: "%dx%dx%d" % s)
+def test_fp8_linear_between(cuda_ok, shape):
+    """Tiles of 16, 32 and 64 tokens, with one piece of the inputs and with several."""
+    tokens, n, k = shape
+    o, got = compare(*shape, out="bf16", seed=3)
+    if tokens % 7 == 0:
+        cm = ops.fp8_linear(*o, channel_major_seqlen=tokens // 7)
+        assert torch.equal(cm, got.view(7, tokens // 7, n).transpose(1, 2))
+
+
 @pytest.mark.parametrize("shape", [(3, 1, 300, 256), (2, 7, 130, 272), (3, 431, 848, 1536), (2, 2050, 1400, 384)],
                          ids=lambda s: "%dx%dx%dx%d" % s)
 @pytest.mark.parametrize("out", ["bf16", "fp32"])
