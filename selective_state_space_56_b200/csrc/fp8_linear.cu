@@ -742,7 +742,9 @@ token_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUt
             }
         }
     }
-    cluster_sync();  // a CTA's shared memory outlives its peers' reads
+    // A CTA's shared memory outlives its peers' reads.  They are done (their values were used), so the
+    // arrival need not wait for the outputs' way to memory as a releasing one does.
+    asm volatile("barrier.cluster.arrive.relaxed.aligned;\nbarrier.cluster.wait.aligned;" ::: "memory");
 }
 
 // ---- host ------------------------------------------------------------------------------
