@@ -108,6 +108,34 @@ def test_gated_scan_rows_by_teams(cuda_ok, rows, L):
     compare(problem(1, rows, L, "bf16", rows % 2 == 0, seed=rows), "bf16", rows % 2 == 0)
 
 
+@pytest.mark.parametrize("decay", [False, True], ids=["sigmoid", "decay"])
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("z", [False, True], ids=["no_z", "z"])
+@pytest.mark.parametrize("rows,L", [(1186, 513), (1203, 1029), (1190, 1536), (60, 2605)])
+def test_gated_scan_chunks_ahead(cuda_ok, rows, L, z, dtype, decay):
+    """Rows of more chunks than a warp keeps on their way, walked alone and by teams."""
+    compare(problem(1, rows, L, dtype, decay, z=z, seed=rows), dtype, decay)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("rows,L", [(1190, 777), (1190, 41), (40, 1541)])
+def test_gated_scan_nan_stays_in_its_row(cuda_ok, rows, L, dtype):
+    """Vectors that two rows share: what one row holds there does not reach the other."""
+    p = dev(problem(1, rows, L, dtype, False, bias=False, seed=5))
+    bad = {k: None if v is None else v.clone() for k, v in p.items()}
+    for k in ("x", "gate", "z", "dy"):
+        bad[k][0, 7] = float("nan")
+    keep = [i for i in range(rows) if i != 7]
+    out = []
+    for c in (p, bad):
+        y, last = ops.gated_scan_fwd(c["x"], c["gate"], None, c["z"], c["h0"], return_last_state=True)
+        g = ops.gated_scan_bwd(c["x"], c["gate"], c["dy"], None, c["z"], c["h0"], c["dlast"])
+        out.append([y, last, g["dx"], g["dgate"], g["dz"], g["dinitial_state"]])
+    for clean, got in zip(*out):
+        assert torch.equal(clean[:, keep], got[:, keep])
+    assert torch.isnan(out[1][0][0, 7]).all()
+
+
 def test_gated_scan_gradients_against_differences(cuda_ok):
     """Central differences of the GPU forward (fp32, summed in fp64) in random directions."""
     p = problem(1, 4, 40, "fp32", False, seed=5)
