@@ -566,8 +566,8 @@ int mamba_add_rms_norm_fwd(const void* x, const void* residual, const float* wei
 
 /*
  * The same with the output in e4m3 and a scale for each row and 128 columns, as
- * mamba_fp8_linear takes it: per group scale = max(largest |out|, 1e-30) / 448, q = out / scale
- * rounded to nearest even.
+ * mamba_fp8_linear takes it: per group scale = max(largest |out|, 1e-30) / 448 and q = 448 out /
+ * max(largest |out|, 1e-30), that quotient rounded to nearest even.
  *
  *   q      : (rows, dim) e4m3                          dim a multiple of 16
  *   scales : (rows, ceil(dim / 128)) float32

@@ -132,9 +132,14 @@ __global__ void __launch_bounds__(ALONE ? 32 * kAloneWarps : kMaxThreads) norm_k
             for (int s = 8; s > 0; s >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, s));
             if (in) {
                 const float top = m * rstd;  // the group's largest output
-                const float inv = top >= kAmaxFloor ? kE4m3Max / m : rstd * (kE4m3Max / kAmaxFloor);
+                if (top >= kAmaxFloor) {
+                    const Quotient by(m);
+                    by(o);
+                } else {
+                    const float inv = rstd * (kE4m3Max / kAmaxFloor);
 #pragma unroll
-                for (int j = 0; j < kE; ++j) o[j] *= inv;
+                    for (int j = 0; j < kE; ++j) o[j] *= inv;
+                }
                 *reinterpret_cast<uint2*>(static_cast<uint8_t*>(p.out) + e) = to_e4m3(o);
                 const int64_t c = e - w.lo, groups = (p.dim + kGroup - 1) / kGroup;
                 if (c % kGroup == 0)
@@ -388,9 +393,8 @@ __global__ void __launch_bounds__(256) quantize_kernel(const T* x, uint8_t* q, f
         for (int s = 8; s > 0; s >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, s));
         m = fmaxf(m, kAmaxFloor);
         if (at[i] < 0) continue;
-        const float inv = kE4m3Max / m;
-#pragma unroll
-        for (int j = 0; j < kE; ++j) v[j] *= inv;
+        const Quotient by(m);
+        by(v);
         *reinterpret_cast<uint2*>(q + at[i]) = to_e4m3(v);
         if (lane == 0) scales[g0 + i * 16] = m / kE4m3Max;
     }
@@ -411,6 +415,7 @@ template <> struct Pair<__nv_bfloat16> {
     __device__ __forceinline__ static Pair zero() { return {__floats2bfloat162_rn(0.f, 0.f)}; }
     __device__ __forceinline__ void max_abs(Pair w) { v = __hmax2(v, __habs2(w.v)); }
     __device__ __forceinline__ float2 f() const { return __bfloat1622float2(v); }
+    __device__ __forceinline__ f2 packed() const { return bf16pair(*reinterpret_cast<const uint32_t*>(&v)); }
 };
 template <> struct Pair<float> {
     float2 v;
@@ -418,6 +423,7 @@ template <> struct Pair<float> {
     __device__ __forceinline__ static Pair zero() { return {make_float2(0.f, 0.f)}; }
     __device__ __forceinline__ void max_abs(Pair w) { v = make_float2(fmaxf(v.x, fabsf(w.v.x)), fmaxf(v.y, fabsf(w.v.y))); }
     __device__ __forceinline__ float2 f() const { return v; }
+    __device__ __forceinline__ f2 packed() const { return pack2(v.x, v.y); }
 };
 
 // ALIGNED: rows begin at vector boundaries (L a multiple of the vector), so all shifts are zero
@@ -480,19 +486,20 @@ __global__ void __launch_bounds__(256, sizeof(T) == 2 ? 6 : 4) quantize_cm_kerne
     float m0 = kAmaxFloor, m1 = kAmaxFloor;
 #pragma unroll
     for (int i = 0; i < 8; ++i) m0 = fmaxf(m0, mx[i][t / 2].x), m1 = fmaxf(m1, mx[i][t / 2].y);
-    const float i0 = kE4m3Max / m0, i1 = kE4m3Max / m1;
     // piece `part` of token r at place part ^ (r / 2 % 8) of its 128 bytes: no bank conflicts
     // where it is written (every second token) and none where it is read (whole tokens)
     uint8_t* staged = reinterpret_cast<uint8_t*>(tile);
     {
-        float v[16];
+        const Quotient by(m0, m1);
         uint8_t* at = staged + t * kGroup + ((part ^ (t / 2 & 7)) * 16);
 #pragma unroll
-        for (int i = 0; i < 16; ++i) v[i] = w[i].f().x;
-        *reinterpret_cast<uint4*>(at) = to_e4m3(v, i0);
+        for (int i = 0; i < 16; i += kE) {
+            float v0[kE], v1[kE];
 #pragma unroll
-        for (int i = 0; i < 16; ++i) v[i] = w[i].f().y;
-        *reinterpret_cast<uint4*>(at + kGroup) = to_e4m3(v, i1);
+            for (int j = 0; j < kE; ++j) unpack2(by(w[i + j].packed()), v0[j], v1[j]);
+            *reinterpret_cast<uint2*>(at + i) = to_e4m3(v0);
+            *reinterpret_cast<uint2*>(at + kGroup + i) = to_e4m3(v1);
+        }
     }
     if (part == 0) {
         const int64_t groups = (dim + kGroup - 1) / kGroup;
@@ -536,14 +543,13 @@ __global__ void __launch_bounds__(256) quantize_weight_kernel(const T* w, uint8_
 #pragma unroll
     for (int i = 1; i < 8; ++i) m = fmaxf(m, mx[i]);
     m = fmaxf(m, kAmaxFloor);
-    const float inv = kE4m3Max / m;
+    const Quotient by(m);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
         if (r >= n || c + i * kE >= k) continue;
         float v[kE];
         raw[i].to_f(v);
-#pragma unroll
-        for (int j = 0; j < kE; ++j) v[j] *= inv;
+        by(v);
         *reinterpret_cast<uint2*>(q + r * k + c + i * kE) = to_e4m3(v);
     }
     if (threadIdx.x == 0) scales[(int64_t)blockIdx.y * gridDim.x + blockIdx.x] = m / kE4m3Max;

@@ -116,19 +116,40 @@ __device__ __forceinline__ uint2 to_e4m3(const float (&v)[kE]) {
     return make_uint2((uint32_t)h[0] | ((uint32_t)h[1] << 16), (uint32_t)h[2] | ((uint32_t)h[3] << 16));
 }
 
-// Sixteen, each times `inv`.
-__device__ __forceinline__ uint4 to_e4m3(const float (&v)[16], float inv) {
-    float lo[kE], hi[kE];
-#pragma unroll
-    for (int j = 0; j < kE; ++j) lo[j] = v[j] * inv, hi[j] = v[kE + j] * inv;
-    const uint2 a = to_e4m3(lo), b = to_e4m3(hi);
-    return make_uint4(a.x, a.y, b.x, b.y);
-}
-
-// The scale of a block of values with largest magnitude amax, and its reciprocal.  The floor
-// keeps both finite for blocks of zeros (their e4m3 values are zero).
 constexpr float kE4m3Max = 448.f;
-constexpr float kAmaxFloor = 1e-30f;
-constexpr int kGroup = 128;  // values that share a scale
+constexpr float kAmaxFloor = 1e-30f;  // keeps the scale of a group of zeros positive
+constexpr int kGroup = 128;           // values that share a scale
+
+// 448 v / m for the values v of a group with largest magnitude m.  Where v and m have few bits the
+// quotient is often exactly half way between two values of e4m3, and v * (448 / m), rounded twice,
+// then lies beside it (bf16 groups of normal values: 2.4e-4 of the e4m3 outputs off by a step).  So
+// 448 / m is kept in two pieces (as in Dekker, "A floating-point technique for extending the
+// available precision"): hi = 448 / m rounded, lo = (448 - hi m) / m, whose numerator one fused
+// multiply-add gives exactly.  v hi + v lo is then rounded once, from within 2^-46 of the quotient,
+// so a quotient that fp32 holds comes out exactly.  m infinite: hi = lo = 0, so finite values give 0
+// and infinite ones NaN.
+struct Quotient {
+    f2 hi, lo;
+    // The halves of a pair in groups of their own.
+    __device__ __forceinline__ Quotient(float m0, float m1) {
+        const float h0 = kE4m3Max / m0, h1 = kE4m3Max / m1;
+        hi = pack2(h0, h1);
+        lo = pack2(rest(h0, m0), rest(h1, m1));
+    }
+    __device__ __forceinline__ explicit Quotient(float m) {
+        const float h = kE4m3Max / m, l = rest(h, m);
+        hi = pack2(h, h);
+        lo = pack2(l, l);
+    }
+    __device__ __forceinline__ static float rest(float h, float m) {
+        return fmaf(-h, fminf(m, 3e38f), kE4m3Max) * (h * (1.f / kE4m3Max));
+    }
+    __device__ __forceinline__ f2 operator()(f2 v) const { return fma2(v, hi, mul2(v, lo)); }
+    // Eight values of a group, in place.
+    __device__ __forceinline__ void operator()(float (&v)[kE]) const {
+#pragma unroll
+        for (int i = 0; i < kE; i += 2) unpack2((*this)(pack2(v[i], v[i + 1])), v[i], v[i + 1]);
+    }
+};
 
 }  // namespace s6
