@@ -4,8 +4,10 @@
 // through the interpreter took 5 to 10 us a call on top of the launch.  These functions do the same
 // checks and allocations on the C++ side of torch and forward to the same C entry points, whose
 // addresses ops.py hands over (bind).  Whatever is not plainly in order -- another dtype, shape,
-// device or layout, a status other than MAMBA_OK -- makes them return None, and ops.py's own path
-// then finds out what is wrong and says so.  No arithmetic, no state but the addresses.
+// device or layout -- makes them return None before anything is called, and ops.py's own path
+// then finds out what is wrong and says so.  Once the library has been called there is no second
+// call (the update works in place): a status other than MAMBA_OK is raised as MambaError, and so is
+// whatever else goes wrong from there on.  No arithmetic, no state but the addresses and that class.
 #include <Python.h>
 
 #include <ATen/core/Tensor.h>
@@ -31,6 +33,7 @@ struct Calls {
 };
 Calls calls;
 bool bound = false;
+PyObject* error_class = nullptr;  // ops.MambaError(status, name of the call)
 
 constexpr at::ScalarType kF32 = at::kFloat, kE4m3 = at::kFloat8_e4m3fn;
 
@@ -82,8 +85,25 @@ struct Args {
 
 float* f32(void* p) { return static_cast<float*>(p); }
 PyObject* none() { Py_RETURN_NONE; }
-PyObject* wrap(const at::Tensor& t) { return THPVariable_Wrap(t); }
 
+// What follows runs after the library's call and so reports its failures as exceptions.
+PyObject* failed(int status, const char* name) {
+    PyObject* e = PyObject_CallFunction(error_class, "is", status, name);
+    if (e) {
+        PyErr_SetObject(error_class, e);
+        Py_DECREF(e);
+    }
+    return nullptr;
+}
+PyObject* wrap(const at::Tensor& t) noexcept {
+    PyObject* o = nullptr;
+    try {
+        o = THPVariable_Wrap(t);
+    } catch (...) {
+    }
+    if (!o && !PyErr_Occurred()) PyErr_NoMemory();
+    return o;
+}
 PyObject* tuple(std::initializer_list<PyObject*> items) {
     PyObject* r = PyTuple_New((Py_ssize_t)items.size());
     Py_ssize_t i = 0;
@@ -96,8 +116,7 @@ PyObject* tuple(std::initializer_list<PyObject*> items) {
     }
     if (whole) return r;
     Py_XDECREF(r);
-    PyErr_Clear();
-    return none();
+    return nullptr;
 }
 PyObject* or_none(const at::Tensor& t) { return t.defined() ? wrap(t) : none(); }
 
@@ -113,9 +132,9 @@ PyObject* gated_state_update(PyObject* const* o) {
          *z = a.maybe(o[4], dt, shape);
     if (!a.ok || code < 0) return none();
     const at::Tensor y = a.empty(shape, dt);
-    if (calls.mamba_gated_state_update(f32(s->data_ptr()), xp, g, f32(b), z, y.data_ptr(), shape[0], shape[1],
-                                       (mamba_dtype)code, (unsigned)PyLong_AsLong(o[5]), a.stream()) != MAMBA_OK)
-        return none();
+    const int rc = calls.mamba_gated_state_update(f32(s->data_ptr()), xp, g, f32(b), z, y.data_ptr(), shape[0], shape[1],
+                                       (mamba_dtype)code, (unsigned)PyLong_AsLong(o[5]), a.stream());
+    if (rc != MAMBA_OK) return failed(rc, "mamba_gated_state_update");
     return wrap(y);
 }
 
@@ -136,11 +155,11 @@ PyObject* gated_scan_fwd(PyObject* const* o) {
     const at::Tensor y = a.empty(shape, dt);
     at::Tensor last;
     if (o[7] == Py_True) last = a.empty(rows, kF32);
-    if (calls.mamba_gated_scan_fwd(x->data_ptr(), g, f32(b), z, f32(h0), y.data_ptr(),
+    const int rc = calls.mamba_gated_scan_fwd(x->data_ptr(), g, f32(b), z, f32(h0), y.data_ptr(),
                                    last.defined() ? f32(last.data_ptr()) : nullptr, f32(ck), ck_bytes,
                                    {shape[0], shape[1], shape[2]}, (mamba_dtype)code, (mamba_dtype)code,
-                                   (unsigned)PyLong_AsLong(o[6]), a.stream()) != MAMBA_OK)
-        return none();
+                                   (unsigned)PyLong_AsLong(o[6]), a.stream());
+    if (rc != MAMBA_OK) return failed(rc, "mamba_gated_scan_fwd");
     return tuple({wrap(y), or_none(last)});
 }
 
@@ -167,11 +186,11 @@ PyObject* gated_scan_bwd(PyObject* const* o) {
     if (z) dz = a.empty(shape, dt);
     if (b && !(flags & MAMBA_FLAG_GIVEN_DECAY)) db = a.empty(shape[1], kF32);
     if (need > 0) ws = a.empty(need, at::kByte);
-    if (calls.mamba_gated_scan_bwd(x->data_ptr(), g, f32(b), z, f32(h0), dy, f32(dl), dx.data_ptr(), dg.data_ptr(),
+    const int rc = calls.mamba_gated_scan_bwd(x->data_ptr(), g, f32(b), z, f32(h0), dy, f32(dl), dx.data_ptr(), dg.data_ptr(),
                                    dz.defined() ? dz.data_ptr() : nullptr, db.defined() ? f32(db.data_ptr()) : nullptr,
                                    f32(dh0.data_ptr()), f32(ck), ck_bytes, dims, (mamba_dtype)code,
-                                   need > 0 ? ws.data_ptr() : nullptr, (size_t)need, flags, a.stream()) != MAMBA_OK)
-        return none();
+                                   need > 0 ? ws.data_ptr() : nullptr, (size_t)need, flags, a.stream());
+    if (rc != MAMBA_OK) return failed(rc, "mamba_gated_scan_bwd");
     return tuple({wrap(dx), wrap(dg), or_none(dz), or_none(db), wrap(dh0)});
 }
 
@@ -215,10 +234,10 @@ PyObject* add_rms_norm_fwd(PyObject* const* o) {
     const at::Tensor out = a.empty(n.shape, n.dt);
     at::Tensor v;
     if (o[2] != Py_None) v = a.empty(n.shape, n.rt);
-    if (calls.mamba_add_rms_norm_fwd(n.x->data_ptr(), n.residual, f32(n.weight), (float)eps, out.data_ptr(),
+    const int rc = calls.mamba_add_rms_norm_fwd(n.x->data_ptr(), n.residual, f32(n.weight), (float)eps, out.data_ptr(),
                                      v.defined() ? v.data_ptr() : nullptr, n.rows, n.dim, (mamba_dtype)n.code,
-                                     (mamba_dtype)n.rcode, (mamba_dtype)n.code, a.stream()) != MAMBA_OK)
-        return none();
+                                     (mamba_dtype)n.rcode, (mamba_dtype)n.code, a.stream());
+    if (rc != MAMBA_OK) return failed(rc, "mamba_add_rms_norm_fwd");
     return tuple({wrap(out), or_none(v)});
 }
 
@@ -234,10 +253,10 @@ PyObject* add_rms_norm_fp8(PyObject* const* o) {
     const at::Tensor q = a.empty(n.shape, kE4m3), s = a.empty(at::IntArrayRef(groups, n.shape.size()), kF32);
     at::Tensor v;
     if (o[2] != Py_None) v = a.empty(n.shape, n.rt);
-    if (calls.mamba_add_rms_norm_fp8(n.x->data_ptr(), n.residual, f32(n.weight), (float)eps, q.data_ptr(),
+    const int rc = calls.mamba_add_rms_norm_fp8(n.x->data_ptr(), n.residual, f32(n.weight), (float)eps, q.data_ptr(),
                                      f32(s.data_ptr()), v.defined() ? v.data_ptr() : nullptr, n.rows, n.dim,
-                                     (mamba_dtype)n.code, (mamba_dtype)n.rcode, a.stream()) != MAMBA_OK)
-        return none();
+                                     (mamba_dtype)n.code, (mamba_dtype)n.rcode, a.stream());
+    if (rc != MAMBA_OK) return failed(rc, "mamba_add_rms_norm_fp8");
     return tuple({wrap(q), wrap(s), or_none(v)});
 }
 
@@ -254,11 +273,11 @@ PyObject* add_rms_norm_bwd(PyObject* const* o) {
     at::Tensor dres, ws;
     if (n.rt != n.dt) dres = a.empty(n.shape, n.rt);
     if (need > 0) ws = a.empty(need, at::kByte);
-    if (calls.mamba_add_rms_norm_bwd(n.x->data_ptr(), n.residual, f32(n.weight), ds, (float)eps, dx.data_ptr(),
+    const int rc = calls.mamba_add_rms_norm_bwd(n.x->data_ptr(), n.residual, f32(n.weight), ds, (float)eps, dx.data_ptr(),
                                      dres.defined() ? dres.data_ptr() : nullptr, f32(dw.data_ptr()), n.rows, n.dim,
                                      (mamba_dtype)n.code, (mamba_dtype)n.rcode, need > 0 ? ws.data_ptr() : nullptr,
-                                     (size_t)need, a.stream()) != MAMBA_OK)
-        return none();
+                                     (size_t)need, a.stream());
+    if (rc != MAMBA_OK) return failed(rc, "mamba_add_rms_norm_bwd");
     return tuple({wrap(dx), or_none(dres), wrap(dw)});
 }
 
@@ -274,9 +293,9 @@ PyObject* fp8_quantize(PyObject* const* o) {
     const int64_t b = cm ? in[0] : 1, d = in[1], len = cm ? in[2] : in[0];
     const int64_t qs[2] = {b * len, d}, ss[2] = {b * len, (d + 127) / 128};
     const at::Tensor q = a.empty(qs, kE4m3), s = a.empty(ss, kF32);
-    if (calls.mamba_fp8_quantize(x->data_ptr(), q.data_ptr(), f32(s.data_ptr()), b, d, len, cm ? 1 : 0,
-                                 (mamba_dtype)code, a.stream()) != MAMBA_OK)
-        return none();
+    const int rc = calls.mamba_fp8_quantize(x->data_ptr(), q.data_ptr(), f32(s.data_ptr()), b, d, len, cm ? 1 : 0,
+                                 (mamba_dtype)code, a.stream());
+    if (rc != MAMBA_OK) return failed(rc, "mamba_fp8_quantize");
     return tuple({wrap(q), wrap(s)});
 }
 
@@ -295,22 +314,22 @@ PyObject* fp8_linear(PyObject* const* o) {
     const at::ScalarType dt = code == MAMBA_F32 ? at::kFloat : at::kBFloat16;
     const int64_t rows[2] = {t, n}, cols[3] = {len > 0 ? t / len : 0, n, len};
     const at::Tensor out = len > 0 ? a.empty(cols, dt) : a.empty(rows, dt);
-    if (calls.mamba_fp8_linear(x->data_ptr(), f32(xs), wp, f32(ws), out.data_ptr(), t, n, k, len, (mamba_dtype)code,
-                               a.stream()) != MAMBA_OK)
-        return none();
+    const int rc = calls.mamba_fp8_linear(x->data_ptr(), f32(xs), wp, f32(ws), out.data_ptr(), t, n, k, len, (mamba_dtype)code,
+                               a.stream());
+    if (rc != MAMBA_OK) return failed(rc, "mamba_fp8_linear");
     return wrap(out);
 }
 
 // Number of arguments, nothing thrown past the interpreter's boundary.
 template <PyObject* (*F)(PyObject* const*), Py_ssize_t N>
 PyObject* entry(PyObject*, PyObject* const* args, Py_ssize_t n) {
-    if (n != N || !bound) {
-        PyErr_SetString(PyExc_TypeError, "wrong number of arguments, or called before bind()");
+    if (n != N || !bound || !error_class) {
+        PyErr_SetString(PyExc_TypeError, "wrong number of arguments, or called before bind() and set_error()");
         return nullptr;
     }
     try {
         return F(args);
-    } catch (...) {
+    } catch (...) {  // checks and allocations, before the call
         PyErr_Clear();
         return none();
     }
@@ -334,6 +353,13 @@ PyObject* bind(PyObject*, PyObject* names) {
     Py_RETURN_NONE;
 }
 
+// set_error(class): what a failed call raises, made from its status and its name.
+PyObject* set_error(PyObject*, PyObject* cls) {
+    Py_INCREF(cls);
+    Py_XSETREF(error_class, cls);
+    Py_RETURN_NONE;
+}
+
 PyObject* names(PyObject*, PyObject*) {
     PyObject* r = PyList_New(0);
 #define X(name)                                                 \
@@ -349,6 +375,7 @@ PyObject* names(PyObject*, PyObject*) {
 
 #define FAST(f, n) {#f, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(entry<f, n>)), METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {{"bind", bind, METH_O, nullptr},
+                         {"set_error", set_error, METH_O, nullptr},
                          {"names", names, METH_NOARGS, nullptr},
                          FAST(gated_state_update, 6),
                          FAST(gated_scan_fwd, 8),

@@ -59,6 +59,7 @@ def _load_native(lib):
         return None
     if mod.torch_version != torch.__version__:
         return None
+    mod.set_error(MambaError)
     mod.bind({n: ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in mod.names()})
     return mod
 
