@@ -34,7 +34,7 @@ bool dims_ok(int64_t batch, int64_t dim, int64_t dstate, int64_t L) {
     return (bd + 31) / 32 <= (int64_t)0x7fffffff;
 }
 
-int cuda_status(cudaError_t e) { return e == cudaSuccess ? MAMBA_OK : MAMBA_ERR_CUDA; }
+int cuda_status(cudaError_t e) { return s6::taken(e) == cudaSuccess ? MAMBA_OK : MAMBA_ERR_CUDA; }
 
 constexpr unsigned kKnownFlags = MAMBA_FLAG_EXACT_ZOH;
 
@@ -550,9 +550,10 @@ int mamba_diag_wait_timeout(int64_t limit_cycles, void* stream) {
 
 int mamba_check_device_error(int clear, void* stream) {
     unsigned word = 0, linear = 0, gated = 0;
-    if (s6::read_device_error(&word, clear != 0, static_cast<cudaStream_t>(stream)) != cudaSuccess ||
-        s6::read_linear_error(&linear, clear != 0, static_cast<cudaStream_t>(stream)) != cudaSuccess ||
-        s6::read_gated_error(&gated, clear != 0, static_cast<cudaStream_t>(stream)) != cudaSuccess)
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (s6::taken(s6::read_device_error(&word, clear != 0, st)) != cudaSuccess ||
+        s6::taken(s6::read_linear_error(&linear, clear != 0, st)) != cudaSuccess ||
+        s6::taken(s6::read_gated_error(&gated, clear != 0, st)) != cudaSuccess)
         return MAMBA_ERR_CUDA;
     return word | linear | gated ? MAMBA_ERR_TIMEOUT : MAMBA_OK;
 }

@@ -14,7 +14,7 @@ constexpr int64_t kGroup = 128;
 
 bool dtype_ok(int dt) { return dt == MAMBA_F32 || dt == MAMBA_BF16; }
 s6::DType to_dtype(int dt) { return dt == MAMBA_BF16 ? s6::DType::BF16 : s6::DType::F32; }
-int cuda_status(cudaError_t e) { return e == cudaSuccess ? MAMBA_OK : MAMBA_ERR_CUDA; }
+int cuda_status(cudaError_t e) { return s6::taken(e) == cudaSuccess ? MAMBA_OK : MAMBA_ERR_CUDA; }
 
 bool all_aligned(std::initializer_list<const void*> ptrs) {
     for (const void* p : ptrs)

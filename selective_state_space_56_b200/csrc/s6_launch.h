@@ -6,6 +6,13 @@
 
 namespace s6 {
 
+// An error on its way to the caller.  The runtime would report it once more to the next launch
+// that asks cudaGetLastError for its own status, after that launch has been made: it is taken here.
+inline cudaError_t taken(cudaError_t e) {
+    if (e != cudaSuccess) cudaGetLastError();
+    return e;
+}
+
 enum class DType : int { F32 = 0, BF16 = 1 };
 
 // Everything one selective-scan call needs, already validated by the ABI layer.

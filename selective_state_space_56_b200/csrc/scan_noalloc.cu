@@ -23,6 +23,7 @@
 #include <mutex>
 
 #include "../../include/mamba_s6.h"
+#include "s6_launch.h"
 
 namespace {
 
@@ -61,7 +62,7 @@ CtxGetCurrent ctx_get_current() {
 // the first use there).
 int scratch_on_current_device(void** out) {
     int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return MAMBA_ERR_CUDA;
+    if (s6::taken(cudaGetDevice(&dev)) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return MAMBA_ERR_CUDA;
     const CtxGetCurrent get_ctx = ctx_get_current();
     if (!get_ctx) return MAMBA_ERR_CUDA;
     CUcontext ctx = nullptr;
@@ -69,7 +70,7 @@ int scratch_on_current_device(void** out) {
     std::lock_guard<std::mutex> guard(g_lock);
     if (!ctx || g_scratch[dev].ctx != ctx || !g_scratch[dev].addr) {
         void* p = nullptr;
-        if (cudaGetSymbolAddress(&p, g_noalloc_scratch) != cudaSuccess || !p) return MAMBA_ERR_CUDA;
+        if (s6::taken(cudaGetSymbolAddress(&p, g_noalloc_scratch)) != cudaSuccess || !p) return MAMBA_ERR_CUDA;
         // the lookup makes the runtime's context current on this thread if none was
         if (get_ctx(&ctx) != CUDA_SUCCESS || !ctx) return MAMBA_ERR_CUDA;
         g_scratch[dev].ctx = ctx;
