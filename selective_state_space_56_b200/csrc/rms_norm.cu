@@ -342,10 +342,11 @@ __global__ void __launch_bounds__(256) dweight_kernel(const float* part, float* 
     const int cx = threadIdx.x & 7, ry = threadIdx.x >> 3;
     const int64_t c = (int64_t)blockIdx.x * 8 + cx;
     float v = 0.f;
-    cudaGridDependencySynchronize();  // launched early: wait for the shares
+    cudaGridDependencySynchronize();  // launched early: wait for the shares, which no read-only
+                                      // load may fetch: they are written while this kernel runs
     if (c < dim)
 #pragma unroll 8
-        for (int64_t r = ry; r < blocks; r += 32) v += __ldg(part + r * dim + c);
+        for (int64_t r = ry; r < blocks; r += 32) v += part[r * dim + c];
     red[ry][cx] = v;
     __syncthreads();
     if (ry == 0 && c < dim) {
