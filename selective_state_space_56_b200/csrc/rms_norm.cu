@@ -132,14 +132,16 @@ __global__ void __launch_bounds__(ALONE ? 32 * kAloneWarps : kMaxThreads) norm_k
             for (int s = 8; s > 0; s >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, s));
             if (in) {
                 const float top = m * rstd;  // the group's largest output
-                if (top >= kAmaxFloor) {
-                    const Quotient by(m);
-                    by(o);
-                } else {
-                    const float inv = rstd * (kE4m3Max / kAmaxFloor);
+                float largest = m;
+                // rstd goes into the values where without it they, or with it the outputs, are so small
+                // that the quotient's factors would leave fp32's range (groups of zeros; small eps)
+                if (!(m >= kAmaxFloor && top >= kAmaxFloor)) {
+                    largest = fmaxf(top, kAmaxFloor);
 #pragma unroll
-                    for (int j = 0; j < kE; ++j) o[j] *= inv;
+                    for (int j = 0; j < kE; ++j) o[j] *= rstd;
                 }
+                const Quotient by(largest);
+                by(o);
                 *reinterpret_cast<uint2*>(static_cast<uint8_t*>(p.out) + e) = to_e4m3(o);
                 const int64_t c = e - w.lo, groups = (p.dim + kGroup - 1) / kGroup;
                 if (c % kGroup == 0)
