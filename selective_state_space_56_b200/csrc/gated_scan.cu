@@ -54,27 +54,47 @@ __device__ __forceinline__ f2 sigmoid2(f2 t) {
 }
 __device__ __forceinline__ f2 twice(float v) { return pack2(v, v); }
 
-// The lane's 8 steps (a_j, b_j), two at a time in packed arithmetic; nbias = -bias log2(e).
+// A pair of gates: sg = sigmoid(v) and a = 1 - sg, the arguments given as t = -v log2(e).  With e = 2^t,
+// sg = 1 / (1 + e), and a is formed from whichever keeps it exact: 1 - sg while sg is the smaller (one
+// rounding of a number near one), e sg while a is (1 - sg would leave it the rounding of sg, and
+// nothing beyond v = 17).
+__device__ __forceinline__ f2 gate2(f2 t, float& a0, float& a1) {
+    const f2 e = ex2x2(t);
+    float d0, d1, k0, k1, o0, o1;
+    unpack2(add2(e, pack2(1.f, 1.f)), d0, d1);
+    const float s0 = rcp(d0), s1 = rcp(d1);
+    const f2 sg = pack2(s0, s1);
+    unpack2(sub2(twice(1.f), sg), k0, k1);
+    unpack2(mul2(e, sg), o0, o1);
+    a0 = s0 < 0.5f ? k0 : o0;
+    a1 = s1 < 0.5f ? k1 : o1;
+    return sg;
+}
+
+// The lane's 8 decays a_j and (sigmoid form) sigmoids sg_j, two at a time in packed arithmetic;
+// nbias = -bias log2(e).
 template <bool DECAY, typename T>
-__device__ __forceinline__ void steps(const Raw8<T>& x, const Raw8<T>& g, float nbias, float (&a)[kE],
-                                      float (&b)[kE]) {
+__device__ __forceinline__ void decays(const Raw8<T>& g, float nbias, float (&a)[kE], float (&sg)[kE]) {
 #pragma unroll
     for (int i = 0; i < kE / 2; ++i) {
-        f2 av = g.pair(i), bv = x.pair(i);
-        if (!DECAY) {
-            const f2 s = sigmoid2(fma2(av, twice(-kLog2e), twice(nbias)));
-            av = sub2(twice(1.f), s);
-            bv = mul2(s, bv);
-        }
-        unpack2(av, a[2 * i], a[2 * i + 1]);
-        unpack2(bv, b[2 * i], b[2 * i + 1]);
+        if (DECAY) unpack2(g.pair(i), a[2 * i], a[2 * i + 1]);
+        else unpack2(gate2(fma2(g.pair(i), twice(-kLog2e), twice(nbias)), a[2 * i], a[2 * i + 1]), sg[2 * i], sg[2 * i + 1]);
     }
 }
-// Steps outside the row become the identity.
-__device__ __forceinline__ void mask_steps(int64_t e, const Row& w, float (&a)[kE], float (&b)[kE]) {
+// Its inputs b_j.
+template <bool DECAY, typename T>
+__device__ __forceinline__ void inputs(const Raw8<T>& x, const float (&sg)[kE], float (&b)[kE]) {
+#pragma unroll
+    for (int i = 0; i < kE / 2; ++i) {
+        const f2 v = DECAY ? x.pair(i) : mul2(pack2(sg[2 * i], sg[2 * i + 1]), x.pair(i));
+        unpack2(v, b[2 * i], b[2 * i + 1]);
+    }
+}
+// Steps outside the row become the identity: a = 1, b = 0.
+__device__ __forceinline__ void outside(int64_t e, const Row& w, float (&v)[kE], float value) {
 #pragma unroll
     for (int j = 0; j < kE; ++j)
-        if (e + j < w.lo || e + j >= w.hi) a[j] = 1.f, b[j] = 0.f;
+        if (e + j < w.lo || e + j >= w.hi) v[j] = value;
 }
 
 // Inclusive scan over the lanes of the compositions (P, H), earlier lanes first.  (The shuffle's
@@ -344,8 +364,9 @@ __global__ void __launch_bounds__(TEAM ? 32 * kTeamWarps : 32 * kWarps, TEAM ? 4
             }
         }
         float a[kE], b[kE];
-        steps<DECAY>(xr, gr, nbias, a, b);
-        if (edge) mask_steps(e, w, a, b);
+        decays<DECAY>(gr, nbias, a, b);
+        inputs<DECAY>(xr, b, b);
+        if (edge) outside(e, w, a, 1.f), outside(e, w, b, 0.f);
         float P = a[0], H = b[0];
 #pragma unroll
         for (int j = 1; j < kE; ++j) {
@@ -476,9 +497,9 @@ __global__ void __launch_bounds__(TEAM ? 32 * kTeamWarps : 32 * kWarps, TEAM ? 1
                 if (GATED) get<T>(zn, p.z, en, w, edge_n);
             }
         }
-        float a[kE], b[kE], gy[kE], dz[kE];
-        steps<DECAY>(xr, gr, nbias, a, b);
-        if (edge) mask_steps(e, w, a, b);
+        float a[kE], sg[kE], gy[kE], dz[kE];
+        decays<DECAY>(gr, nbias, a, sg);
+        if (edge) outside(e, w, a, 1.f);
 #pragma unroll
         for (int i = 0; i < kE / 2; ++i) {
             f2 g = yr.pair(i);
@@ -490,11 +511,7 @@ __global__ void __launch_bounds__(TEAM ? 32 * kTeamWarps : 32 * kWarps, TEAM ? 1
             }
             unpack2(g, gy[2 * i], gy[2 * i + 1]);
         }
-        if (edge) {
-#pragma unroll
-            for (int j = 0; j < kE; ++j)
-                if (e + j < w.lo || e + j >= w.hi) gy[j] = 0.f;
-        }
+        if (edge) outside(e, w, gy, 0.f);
         float P = 1.f, E = 0.f;
 #pragma unroll
         for (int j = kE - 1; j >= 0; --j) {
@@ -510,7 +527,9 @@ __global__ void __launch_bounds__(TEAM ? 32 * kTeamWarps : 32 * kWarps, TEAM ? 1
         if (lane == 31) ev = in;
         if (!TEAM) ec = __shfl_sync(kFull, after, 0);
         if (TEAM && c >= chunks) continue;
-        float hv[kE];  // the state before each step
+        float b[kE], hv[kE];  // inputs (formed here, so that the sigmoids alone wait for the gradients), states before each step
+        inputs<DECAY>(xr, sg, b);
+        if (edge) outside(e, w, b, 0.f);
         {
             float H = b[0];
 #pragma unroll
@@ -540,7 +559,7 @@ __global__ void __launch_bounds__(TEAM ? 32 * kTeamWarps : 32 * kWarps, TEAM ? 1
                 unpack2(mul2(d, hp), dg[2 * i], dg[2 * i + 1]);
             } else {
                 const f2 av = pack2(a[2 * i], a[2 * i + 1]);
-                const f2 dx = mul2(sub2(twice(1.f), av), d);
+                const f2 dx = mul2(pack2(sg[2 * i], sg[2 * i + 1]), d);
                 unpack2(dx, dh[2 * i], dh[2 * i + 1]);
                 unpack2(mul2(mul2(dx, sub2(xr.pair(i), hp)), av), dg[2 * i], dg[2 * i + 1]);
             }
@@ -548,11 +567,7 @@ __global__ void __launch_bounds__(TEAM ? 32 * kTeamWarps : 32 * kWarps, TEAM ? 1
         set<T>(q.dx, e, w, edge, dh);
         set<T>(q.dg, e, w, edge, dg);
         if (!DECAY) {
-            if (edge) {
-#pragma unroll
-                for (int j = 0; j < kE; ++j)
-                    if (e + j < w.lo || e + j >= w.hi) dg[j] = 0.f;
-            }
+            if (edge) outside(e, w, dg, 0.f);
             bsum += ((dg[0] + dg[1]) + (dg[2] + dg[3])) + ((dg[4] + dg[5]) + (dg[6] + dg[7]));
         }
     }
@@ -635,8 +650,8 @@ __global__ void __launch_bounds__(128) gated_update_kernel(float* state, const T
         if (DECAY) {
             h[j] = fmaf(gf, h[j], xf);
         } else {
-            const float s = rcp(1.f + ex2(fmaf(gf, -kLog2e, -kLog2e * b[j])));
-            h[j] = fmaf(1.f - s, h[j], s * xf);
+            const float e = ex2(fmaf(gf, -kLog2e, -kLog2e * b[j])), s = rcp(1.f + e);
+            h[j] = fmaf(s < 0.5f ? 1.f - s : e * s, h[j], s * xf);  // as gate2
         }
         yv.v[j] = io<T>::from_f(GATED ? h[j] * silu(io<T>::to_f(zv.v[j])) : h[j]);
     }
