@@ -22,8 +22,9 @@
 //                    a fixed order.
 //
 // Every wait is bounded: one that gives up sets the device error word and the CTA's abort
-// flag, all roles leave their loops, outstanding copies and products are waited for (bounded
-// too), tensor memory is freed and the kernel returns.
+// flag, and all roles leave their loops.  The role that issued copies or products waits for the last
+// of them (bounded too) before the CTA goes on to its end, whichever role gave up and also when none
+// did; then tensor memory is freed and the kernel returns.
 #include <cudaTypedefs.h>
 
 #include <algorithm>
@@ -438,7 +439,9 @@ prefill_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ C
                         used = max(used, s.at + 1);
                     }
                 }
-                if (!ok && rank == 0)  // copies in flight (the last use of each stage) before the end
+                // The pair does not end before the copies into it have (the last use of each stage): a role
+                // that gives up may do so long after the last of them was issued.
+                if (rank == 0)
                     for (int j = 0; j < used; ++j)
                         mbar_wait_bounded(&bars.full[j], j < s.at ? s.phase : s.phase ^ 1u, kLimit / 8);
             }
@@ -465,10 +468,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ C
                         tc_commit_pair(&bars.empty[s.at]);
                     }
                 }
-                if (!ok) {
-                    tc_commit_pair(&bars.drain);
-                    mbar_wait_bounded(&bars.drain, 0, kLimit / 8);
-                }
+                tc_commit_pair(&bars.drain);
             }
         }
     } else {
@@ -537,6 +537,12 @@ prefill_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ C
     }
     tc_fence_before();
     __syncthreads();
+    // ... nor before the products, which read the pair's shared memory, write its tensor memory and
+    // signal both CTAs
+    if (warp == 1) {
+        if (elect_one()) mbar_wait_bounded(&bars.drain, 0, kLimit / 8);
+        __syncwarp();
+    }
     cluster_sync();  // neither CTA ends while the other may still signal it or read its memory
     tc_fence_after();
     if (warp == 2) tmem_free_pair(tmem, 512);
@@ -619,14 +625,12 @@ token_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUt
             int s = 0;
             uint32_t phase = 1;
             for (int k = k0 + ahead; k < k1; ++k) {  // ahead == stages here: stage 0 comes next
-                if (!wait_or_abort(&bars.empty[s], phase ^ 1u, &bars.ctl)) {
-                    for (int j = 0; j < stages; ++j)  // copies in flight
-                        mbar_wait_bounded(&bars.full[j], j < s ? phase : phase ^ 1u, kLimit / 8);
-                    break;
-                }
+                if (!wait_or_abort(&bars.empty[s], phase ^ 1u, &bars.ctl)) break;
                 load(k, s);
                 if (++s == stages) s = 0, phase ^= 1u;
             }
+            // the CTA does not end before the copies into it have (see prefill_kernel)
+            for (int j = 0; j < ahead; ++j) mbar_wait_bounded(&bars.full[j], j < s ? phase : phase ^ 1u, kLimit / 8);
         }
     } else if (warp == 5) {
         if (elect_one()) {
@@ -636,11 +640,8 @@ token_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUt
             Turn<kTurns> d;
             for (int k = k0; k < k1; ++k, d.next()) {
                 if (!wait_or_abort(&bars.free[d.at], d.phase ^ 1u, &bars.ctl) ||
-                    !wait_or_abort(&bars.full[s], phase, &bars.ctl)) {
-                    tc_commit(&bars.drain);
-                    mbar_wait_bounded(&bars.drain, 0, kLimit / 8);
+                    !wait_or_abort(&bars.full[s], phase, &bars.ctl))
                     break;
-                }
                 tc_fence_after();
                 const uint32_t a = smem_addr(ring + (size_t)s * kStage);
                 mma_stage(tmem + d.at * BN, a, a + kBM * kBK, idesc);
@@ -648,6 +649,8 @@ token_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUt
                 tc_commit(&bars.empty[s]);
                 if (++s == stages) s = 0, phase ^= 1u;
             }
+            tc_commit(&bars.drain);  // ... nor before the products
+            mbar_wait_bounded(&bars.drain, 0, kLimit / 8);
         }
     } else {
         // token scales times the tile's weight scales, by block and column, while the tiles load
