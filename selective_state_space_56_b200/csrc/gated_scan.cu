@@ -277,12 +277,16 @@ __device__ __forceinline__ float team_round(Team& team, int round, int ctas, int
             if (lane == 0) team.enter[buf] = carry;
             carry = fmaf(all.x, carry, all.y);
         } else {
-            if (lane == 0) mbar_arrive_expect_tx(&team.here[buf], (uint32_t)ctas * 8u);
-            if (lane < ctas) hand_over(&team.cta[buf][rank], &team.here[buf], (uint32_t)lane, all);
-            __syncwarp();
-            if (alive && !__all_sync(kFull, mbar_wait_bounded(&team.here[buf], (uint32_t)(round >> 1) & 1u, kLimit))) {
-                if (lane == 0) atomicOr(&g_gated_error, 1u);
-                alive = false;  // the outputs are void; the rounds end without further waits
+            // A CTA that gave up takes no further part: its barrier's phase may be incomplete, and a second
+            // arrival in a phase of one is not allowed.  Its peers give up in their turn.
+            if (alive) {
+                if (lane == 0) mbar_arrive_expect_tx(&team.here[buf], (uint32_t)ctas * 8u);
+                if (lane < ctas) hand_over(&team.cta[buf][rank], &team.here[buf], (uint32_t)lane, all);
+                __syncwarp();
+                if (!__all_sync(kFull, mbar_wait_bounded(&team.here[buf], (uint32_t)(round >> 1) & 1u, kLimit))) {
+                    if (lane == 0) atomicOr(&g_gated_error, 1u);
+                    alive = false;  // the outputs are void; the rounds end without further waits
+                }
             }
             P = 1.f, H = 0.f;
             if (lane < ctas) {
