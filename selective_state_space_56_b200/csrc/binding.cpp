@@ -86,6 +86,17 @@ struct Args {
 float* f32(void* p) { return static_cast<float*>(p); }
 PyObject* none() { Py_RETURN_NONE; }
 
+// A call of the library without the interpreter's lock, as ctypes makes it: a launch can wait for room in
+// the launch queue, and what makes room (a host function on a stream, another thread) may need the lock.
+template <typename F>
+int unlocked(F call) {
+    struct Unlock {
+        PyThreadState* thread = PyEval_SaveThread();
+        ~Unlock() { PyEval_RestoreThread(thread); }
+    } unlock;
+    return call();
+}
+
 // What follows runs after the library's call and so reports its failures as exceptions.
 PyObject* failed(int status, const char* name) {
     PyObject* e = PyObject_CallFunction(error_class, "is", status, name);
@@ -125,6 +136,7 @@ PyObject* gated_state_update(PyObject* const* o) {
     Args a;
     const at::Tensor *s = a.first(o[0]), *x = a.plain(o[1]);
     if (!a.ok || s->dim() != 2 || s->scalar_type() != kF32) return none();
+    const unsigned flags = (unsigned)PyLong_AsLong(o[5]);
     const auto shape = s->sizes();
     const auto dt = x->scalar_type();
     const int code = code_of(dt);
@@ -132,8 +144,10 @@ PyObject* gated_state_update(PyObject* const* o) {
          *z = a.maybe(o[4], dt, shape);
     if (!a.ok || code < 0) return none();
     const at::Tensor y = a.empty(shape, dt);
-    const int rc = calls.mamba_gated_state_update(f32(s->data_ptr()), xp, g, f32(b), z, y.data_ptr(), shape[0], shape[1],
-                                       (mamba_dtype)code, (unsigned)PyLong_AsLong(o[5]), a.stream());
+    const int rc = unlocked([&] {
+        return calls.mamba_gated_state_update(f32(s->data_ptr()), xp, g, f32(b), z, y.data_ptr(), shape[0], shape[1],
+                                              (mamba_dtype)code, flags, a.stream());
+    });
     if (rc != MAMBA_OK) return failed(rc, "mamba_gated_state_update");
     return wrap(y);
 }
@@ -146,6 +160,7 @@ PyObject* gated_scan_fwd(PyObject* const* o) {
     const auto shape = x->sizes();
     const auto dt = x->scalar_type();
     const int code = code_of(dt);
+    const unsigned flags = (unsigned)PyLong_AsLong(o[6]);
     const int64_t rows[2] = {shape[0], shape[1]};
     void *g = a.address(o[1], dt, shape), *b = a.maybe(o[2], kF32, shape[1]), *z = a.maybe(o[3], dt, shape),
          *h0 = a.maybe(o[4], kF32, rows);
@@ -155,10 +170,12 @@ PyObject* gated_scan_fwd(PyObject* const* o) {
     const at::Tensor y = a.empty(shape, dt);
     at::Tensor last;
     if (o[7] == Py_True) last = a.empty(rows, kF32);
-    const int rc = calls.mamba_gated_scan_fwd(x->data_ptr(), g, f32(b), z, f32(h0), y.data_ptr(),
-                                   last.defined() ? f32(last.data_ptr()) : nullptr, f32(ck), ck_bytes,
-                                   {shape[0], shape[1], shape[2]}, (mamba_dtype)code, (mamba_dtype)code,
-                                   (unsigned)PyLong_AsLong(o[6]), a.stream());
+    const int rc = unlocked([&] {
+        return calls.mamba_gated_scan_fwd(x->data_ptr(), g, f32(b), z, f32(h0), y.data_ptr(),
+                                          last.defined() ? f32(last.data_ptr()) : nullptr, f32(ck), ck_bytes,
+                                          {shape[0], shape[1], shape[2]}, (mamba_dtype)code, (mamba_dtype)code,
+                                          flags, a.stream());
+    });
     if (rc != MAMBA_OK) return failed(rc, "mamba_gated_scan_fwd");
     return tuple({wrap(y), or_none(last)});
 }
@@ -186,10 +203,12 @@ PyObject* gated_scan_bwd(PyObject* const* o) {
     if (z) dz = a.empty(shape, dt);
     if (b && !(flags & MAMBA_FLAG_GIVEN_DECAY)) db = a.empty(shape[1], kF32);
     if (need > 0) ws = a.empty(need, at::kByte);
-    const int rc = calls.mamba_gated_scan_bwd(x->data_ptr(), g, f32(b), z, f32(h0), dy, f32(dl), dx.data_ptr(), dg.data_ptr(),
-                                   dz.defined() ? dz.data_ptr() : nullptr, db.defined() ? f32(db.data_ptr()) : nullptr,
-                                   f32(dh0.data_ptr()), f32(ck), ck_bytes, dims, (mamba_dtype)code,
-                                   need > 0 ? ws.data_ptr() : nullptr, (size_t)need, flags, a.stream());
+    const int rc = unlocked([&] {
+        return calls.mamba_gated_scan_bwd(x->data_ptr(), g, f32(b), z, f32(h0), dy, f32(dl), dx.data_ptr(), dg.data_ptr(),
+                                          dz.defined() ? dz.data_ptr() : nullptr, db.defined() ? f32(db.data_ptr()) : nullptr,
+                                          f32(dh0.data_ptr()), f32(ck), ck_bytes, dims, (mamba_dtype)code,
+                                          need > 0 ? ws.data_ptr() : nullptr, (size_t)need, flags, a.stream());
+    });
     if (rc != MAMBA_OK) return failed(rc, "mamba_gated_scan_bwd");
     return tuple({wrap(dx), wrap(dg), or_none(dz), or_none(db), wrap(dh0)});
 }
@@ -234,9 +253,11 @@ PyObject* add_rms_norm_fwd(PyObject* const* o) {
     const at::Tensor out = a.empty(n.shape, n.dt);
     at::Tensor v;
     if (o[2] != Py_None) v = a.empty(n.shape, n.rt);
-    const int rc = calls.mamba_add_rms_norm_fwd(n.x->data_ptr(), n.residual, f32(n.weight), (float)eps, out.data_ptr(),
-                                     v.defined() ? v.data_ptr() : nullptr, n.rows, n.dim, (mamba_dtype)n.code,
-                                     (mamba_dtype)n.rcode, (mamba_dtype)n.code, a.stream());
+    const int rc = unlocked([&] {
+        return calls.mamba_add_rms_norm_fwd(n.x->data_ptr(), n.residual, f32(n.weight), (float)eps, out.data_ptr(),
+                                            v.defined() ? v.data_ptr() : nullptr, n.rows, n.dim, (mamba_dtype)n.code,
+                                            (mamba_dtype)n.rcode, (mamba_dtype)n.code, a.stream());
+    });
     if (rc != MAMBA_OK) return failed(rc, "mamba_add_rms_norm_fwd");
     return tuple({wrap(out), or_none(v)});
 }
@@ -253,9 +274,11 @@ PyObject* add_rms_norm_fp8(PyObject* const* o) {
     const at::Tensor q = a.empty(n.shape, kE4m3), s = a.empty(at::IntArrayRef(groups, n.shape.size()), kF32);
     at::Tensor v;
     if (o[2] != Py_None) v = a.empty(n.shape, n.rt);
-    const int rc = calls.mamba_add_rms_norm_fp8(n.x->data_ptr(), n.residual, f32(n.weight), (float)eps, q.data_ptr(),
-                                     f32(s.data_ptr()), v.defined() ? v.data_ptr() : nullptr, n.rows, n.dim,
-                                     (mamba_dtype)n.code, (mamba_dtype)n.rcode, a.stream());
+    const int rc = unlocked([&] {
+        return calls.mamba_add_rms_norm_fp8(n.x->data_ptr(), n.residual, f32(n.weight), (float)eps, q.data_ptr(),
+                                            f32(s.data_ptr()), v.defined() ? v.data_ptr() : nullptr, n.rows, n.dim,
+                                            (mamba_dtype)n.code, (mamba_dtype)n.rcode, a.stream());
+    });
     if (rc != MAMBA_OK) return failed(rc, "mamba_add_rms_norm_fp8");
     return tuple({wrap(q), wrap(s), or_none(v)});
 }
@@ -273,10 +296,12 @@ PyObject* add_rms_norm_bwd(PyObject* const* o) {
     at::Tensor dres, ws;
     if (n.rt != n.dt) dres = a.empty(n.shape, n.rt);
     if (need > 0) ws = a.empty(need, at::kByte);
-    const int rc = calls.mamba_add_rms_norm_bwd(n.x->data_ptr(), n.residual, f32(n.weight), ds, (float)eps, dx.data_ptr(),
-                                     dres.defined() ? dres.data_ptr() : nullptr, f32(dw.data_ptr()), n.rows, n.dim,
-                                     (mamba_dtype)n.code, (mamba_dtype)n.rcode, need > 0 ? ws.data_ptr() : nullptr,
-                                     (size_t)need, a.stream());
+    const int rc = unlocked([&] {
+        return calls.mamba_add_rms_norm_bwd(n.x->data_ptr(), n.residual, f32(n.weight), ds, (float)eps, dx.data_ptr(),
+                                            dres.defined() ? dres.data_ptr() : nullptr, f32(dw.data_ptr()), n.rows, n.dim,
+                                            (mamba_dtype)n.code, (mamba_dtype)n.rcode, need > 0 ? ws.data_ptr() : nullptr,
+                                            (size_t)need, a.stream());
+    });
     if (rc != MAMBA_OK) return failed(rc, "mamba_add_rms_norm_bwd");
     return tuple({wrap(dx), or_none(dres), wrap(dw)});
 }
@@ -293,8 +318,10 @@ PyObject* fp8_quantize(PyObject* const* o) {
     const int64_t b = cm ? in[0] : 1, d = in[1], len = cm ? in[2] : in[0];
     const int64_t qs[2] = {b * len, d}, ss[2] = {b * len, (d + 127) / 128};
     const at::Tensor q = a.empty(qs, kE4m3), s = a.empty(ss, kF32);
-    const int rc = calls.mamba_fp8_quantize(x->data_ptr(), q.data_ptr(), f32(s.data_ptr()), b, d, len, cm ? 1 : 0,
-                                 (mamba_dtype)code, a.stream());
+    const int rc = unlocked([&] {
+        return calls.mamba_fp8_quantize(x->data_ptr(), q.data_ptr(), f32(s.data_ptr()), b, d, len, cm ? 1 : 0,
+                                        (mamba_dtype)code, a.stream());
+    });
     if (rc != MAMBA_OK) return failed(rc, "mamba_fp8_quantize");
     return tuple({wrap(q), wrap(s)});
 }
@@ -314,8 +341,10 @@ PyObject* fp8_linear(PyObject* const* o) {
     const at::ScalarType dt = code == MAMBA_F32 ? at::kFloat : at::kBFloat16;
     const int64_t rows[2] = {t, n}, cols[3] = {len > 0 ? t / len : 0, n, len};
     const at::Tensor out = len > 0 ? a.empty(cols, dt) : a.empty(rows, dt);
-    const int rc = calls.mamba_fp8_linear(x->data_ptr(), f32(xs), wp, f32(ws), out.data_ptr(), t, n, k, len, (mamba_dtype)code,
-                               a.stream());
+    const int rc = unlocked([&] {
+        return calls.mamba_fp8_linear(x->data_ptr(), f32(xs), wp, f32(ws), out.data_ptr(), t, n, k, len, (mamba_dtype)code,
+                                      a.stream());
+    });
     if (rc != MAMBA_OK) return failed(rc, "mamba_fp8_linear");
     return wrap(out);
 }
