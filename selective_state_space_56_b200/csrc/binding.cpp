@@ -200,7 +200,7 @@ PyObject* gated_scan_bwd(PyObject* const* o) {
     const int64_t need = (int64_t)calls.mamba_gated_scan_bwd_workspace_size(dims);
     const at::Tensor dx = a.empty(shape, dt), dg = a.empty(shape, dt), dh0 = a.empty(rows, kF32);
     at::Tensor dz, db, ws;
-    if (z) dz = a.empty(shape, dt);
+    if (o[4] != Py_None) dz = a.empty(shape, dt);  // (the address of a z without elements is null)
     if (b && !(flags & MAMBA_FLAG_GIVEN_DECAY)) db = a.empty(shape[1], kF32);
     if (need > 0) ws = a.empty(need, at::kByte);
     const int rc = unlocked([&] {
