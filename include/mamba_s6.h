@@ -661,6 +661,12 @@ int mamba_check_device_error(int clear, void* stream);
 int mamba_diag_wait_timeout(int64_t limit_cycles, void* stream);
 
 /*
+ * The same for the error word of one part of the library: 0 the scans (as above), 1 the
+ * projection, 2 the gated recurrence.  Errors: DIMS (part or limit out of range), CUDA.
+ */
+int mamba_diag_wait_timeout_in(int part, int64_t limit_cycles, void* stream);
+
+/*
  * Diagnostic: evaluates 2^x for n floats three ways on the device -- the FMA-pipe
  * polynomial the scan uses for part of its Abar factors (out_fma), the SFU
  * ex2.approx instruction (out_sfu) and CUDA's exp2f (out_lib) -- so tests can bound

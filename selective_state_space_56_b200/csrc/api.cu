@@ -548,14 +548,28 @@ int mamba_diag_wait_timeout(int64_t limit_cycles, void* stream) {
                                                      static_cast<cudaStream_t>(stream)));
 }
 
+int mamba_diag_wait_timeout_in(int part, int64_t limit_cycles, void* stream) {
+    if (part < 0 || part > 2) return MAMBA_ERR_DIMS;
+    if (part == 0) return mamba_diag_wait_timeout(limit_cycles, stream);
+    if (limit_cycles < 1 || limit_cycles > 4000000000LL) return MAMBA_ERR_DIMS;
+    return cuda_status((part == 1 ? s6::launch_linear_timeout_probe : s6::launch_gated_timeout_probe)(
+        (long long)limit_cycles, static_cast<cudaStream_t>(stream)));
+}
+
 int mamba_check_device_error(int clear, void* stream) {
-    unsigned word = 0, linear = 0, gated = 0;
+    using Read = cudaError_t (*)(unsigned*, bool, cudaStream_t);
+    const Read reads[] = {s6::read_device_error, s6::read_linear_error, s6::read_gated_error};
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    if (s6::taken(s6::read_device_error(&word, clear != 0, st)) != cudaSuccess ||
-        s6::taken(s6::read_linear_error(&linear, clear != 0, st)) != cudaSuccess ||
-        s6::taken(s6::read_gated_error(&gated, clear != 0, st)) != cudaSuccess)
-        return MAMBA_ERR_CUDA;
-    return word | linear | gated ? MAMBA_ERR_TIMEOUT : MAMBA_OK;
+    unsigned words[3] = {0, 0, 0}, any = 0;
+    // every word is read before the first is cleared: a read that fails loses no report
+    for (int i = 0; i < 3; ++i) {
+        if (s6::taken(reads[i](&words[i], false, st)) != cudaSuccess) return MAMBA_ERR_CUDA;
+        any |= words[i];
+    }
+    // a word that could not be cleared is reported again by the next call
+    for (int i = 0; i < 3; ++i)
+        if (clear && words[i]) s6::taken(reads[i](&words[i], true, st));
+    return any ? MAMBA_ERR_TIMEOUT : MAMBA_OK;
 }
 
 const char* mamba_status_string(int status) {
@@ -573,6 +587,6 @@ const char* mamba_status_string(int status) {
     }
 }
 
-int mamba_abi_version(void) { return 106; }
+int mamba_abi_version(void) { return 107; }
 
 }  // extern "C"

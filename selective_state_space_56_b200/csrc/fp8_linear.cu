@@ -937,11 +937,26 @@ cudaError_t run_linear(const LinearArgs& a, cudaStream_t s) {
     }
 }
 
+// One bounded wait on a barrier that nothing completes, as mamba_diag_wait_timeout_in describes.
+__global__ void timeout_probe_kernel(long long limit_cycles) {
+    __shared__ uint64_t bar;
+    if (threadIdx.x == 0) {
+        mbar_init(&bar, 1);
+        fence_barrier_init();
+        if (!mbar_wait_bounded(&bar, 0, limit_cycles)) atomicOr(&g_linear_error, 1u);
+    }
+}
+
 }  // namespace
 
 cudaError_t launch_fp8_linear(const LinearArgs& a, cudaStream_t s) {
     if (a.tokens == 0 || a.n == 0) return cudaSuccess;
     return a.out_dtype == DType::BF16 ? run_linear<__nv_bfloat16>(a, s) : run_linear<float>(a, s);
+}
+
+cudaError_t launch_linear_timeout_probe(long long limit_cycles, cudaStream_t s) {
+    timeout_probe_kernel<<<1, 32, 0, s>>>(limit_cycles);
+    return cudaGetLastError();
 }
 
 cudaError_t read_linear_error(unsigned* out, bool clear, cudaStream_t s) {

@@ -767,6 +767,16 @@ cudaError_t run_update(const GatedUpdateArgs& a, cudaStream_t s) {
     return cudaGetLastError();
 }
 
+// One bounded wait on a barrier that nothing completes, as mamba_diag_wait_timeout_in describes.
+__global__ void timeout_probe_kernel(long long limit_cycles) {
+    __shared__ uint64_t bar;
+    if (threadIdx.x == 0) {
+        mbar_init(&bar, 1);
+        fence_barrier_init();
+        if (!mbar_wait_bounded(&bar, 0, limit_cycles)) atomicOr(&g_gated_error, 1u);
+    }
+}
+
 }  // namespace
 
 // Warps that walk a row: one where there are more than 8 rows an SM (1300 rows of 8192 fp32: 31 us
@@ -841,6 +851,11 @@ cudaError_t launch_gated_scan_bwd(const GatedArgs& a, const GatedBwdArgs& g, cud
 
 cudaError_t launch_gated_update(const GatedUpdateArgs& a, cudaStream_t s) {
     return a.dtype == DType::BF16 ? run_update<__nv_bfloat16>(a, s) : run_update<float>(a, s);
+}
+
+cudaError_t launch_gated_timeout_probe(long long limit_cycles, cudaStream_t s) {
+    timeout_probe_kernel<<<1, 32, 0, s>>>(limit_cycles);
+    return cudaGetLastError();
 }
 
 cudaError_t read_gated_error(unsigned* out, bool clear, cudaStream_t s) {

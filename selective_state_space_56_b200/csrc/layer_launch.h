@@ -58,6 +58,8 @@ cudaError_t launch_gated_scan_bwd(const GatedArgs& a, const GatedBwdArgs& g, cud
 
 // Bit 0 of the recurrence's device error word (a bounded wait gave up), as read_device_error.
 cudaError_t read_gated_error(unsigned* out, bool clear, cudaStream_t stream);
+// One wait of limit_cycles on a barrier that nothing completes; sets that word.
+cudaError_t launch_gated_timeout_probe(long long limit_cycles, cudaStream_t stream);
 
 struct GatedUpdateArgs {
     float* state;  // (batch, dim), updated in place
@@ -135,5 +137,6 @@ struct LinearArgs {
 cudaError_t launch_fp8_linear(const LinearArgs& a, cudaStream_t stream);
 // Bit 0 of the projection's device error word (a bounded wait gave up), as read_device_error.
 cudaError_t read_linear_error(unsigned* out, bool clear, cudaStream_t stream);
+cudaError_t launch_linear_timeout_probe(long long limit_cycles, cudaStream_t stream);  // as for the recurrence
 
 }  // namespace s6

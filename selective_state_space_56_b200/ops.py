@@ -150,6 +150,8 @@ def load_library():
             lib.mamba_check_device_error.argtypes = [i32, vp]
             lib.mamba_diag_wait_timeout.restype = i32
             lib.mamba_diag_wait_timeout.argtypes = [i64, vp]
+            lib.mamba_diag_wait_timeout_in.restype = i32
+            lib.mamba_diag_wait_timeout_in.argtypes = [i32, i64, vp]
             lib.mamba_diag_exp2.restype = i32
             lib.mamba_diag_exp2.argtypes = [vp, vp, vp, vp, i64, vp]
             lib.mamba_diag_throughput.restype = i32
@@ -200,14 +202,15 @@ def check_device_error(clear: bool = True, device=None) -> None:
         raise MambaError(rc, "mamba_check_device_error")
 
 
-def diag_wait_timeout(limit_cycles: int = 2_000_000, device=None) -> None:
+def diag_wait_timeout(limit_cycles: int = 2_000_000, device=None, part: int = 0) -> None:
     """Launch one bounded device wait that nothing completes (it gives up after
-    limit_cycles SM clocks and sets the device error word); for testing detection."""
+    limit_cycles SM clocks and sets the device error word of the scans, part 0, the projection,
+    1, or the gated recurrence, 2); for testing detection."""
     dev = torch.device("cuda", torch.cuda.current_device()) if device is None else device
     with torch.cuda.device(dev):
-        rc = load_library().mamba_diag_wait_timeout(int(limit_cycles), _stream_handle(dev))
+        rc = load_library().mamba_diag_wait_timeout_in(int(part), int(limit_cycles), _stream_handle(dev))
     if rc != 0:
-        raise MambaError(rc, "mamba_diag_wait_timeout")
+        raise MambaError(rc, "mamba_diag_wait_timeout_in")
 
 
 def diag_exp2(x):
