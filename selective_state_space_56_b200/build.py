@@ -9,7 +9,8 @@ statically, so the library loads next to any PyTorch build.  Objects and the
 ``-Xptxas -v`` report go to ``_build/`` at the repository root.
 
 ``csrc/binding.cpp`` (native argument checks and allocations for the layer operators) is
-compiled with g++ against the interpreter's own PyTorch into ``_native.so`` beside it.
+compiled with g++ against the interpreter's own PyTorch into ``_native.so`` beside it.  It is
+optional: where it cannot be built, ``build`` says so and the library is complete without it.
 """
 from __future__ import annotations
 
@@ -21,6 +22,7 @@ import shutil
 import subprocess
 import sys
 import sysconfig
+import warnings
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -83,7 +85,17 @@ def _build_binding(force: bool) -> None:
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
-    _build_binding(force)
+    path = _build_library(force, verbose)
+    try:
+        _build_binding(force)
+    except Exception as e:  # no g++, no torch headers, a torch without CUDA: the library does without
+        if os.path.exists(BINDING_PATH):  # made for other sources
+            os.remove(BINDING_PATH)
+        warnings.warn("%s was not built, its calls go through the interpreter: %s" % (os.path.basename(BINDING_PATH), e))
+    return path
+
+
+def _build_library(force: bool, verbose: bool) -> str:
     if not force and up_to_date():
         return LIB_PATH
     nvcc = _nvcc()
