@@ -9,8 +9,9 @@ statically, so the library loads next to any PyTorch build.  Objects and the
 ``-Xptxas -v`` report go to ``_build/`` at the repository root.
 
 ``csrc/binding.cpp`` (native argument checks and allocations for the layer operators) is
-compiled with g++ against the interpreter's own PyTorch into ``_native.so`` beside it.  It is
-optional: where it cannot be built, ``build`` says so and the library is complete without it.
+compiled with g++ against the interpreter's own PyTorch into ``_native-<its version>.so`` beside
+it, so that another PyTorch gets a binding of its own.  It is optional: where it cannot be built,
+``build`` says so and the library is complete without it.
 """
 from __future__ import annotations
 
@@ -24,6 +25,8 @@ import sys
 import sysconfig
 import warnings
 
+import torch
+
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
@@ -32,7 +35,7 @@ BUILD_DIR = os.path.join(ROOT, "_build")
 LIB_NAME = "libmamba_s6.so"
 LIB_PATH = os.path.join(PKG, LIB_NAME)
 BINDING = os.path.join(CSRC, "binding.cpp")
-BINDING_PATH = os.path.join(PKG, "_native.so")
+BINDING_PATH = os.path.join(PKG, "_native-%s.so" % torch.__version__)
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xptxas", "-v",
@@ -68,7 +71,6 @@ def _build_binding(force: bool) -> None:
     if (not force and os.path.exists(BINDING_PATH)
             and os.path.getmtime(BINDING_PATH) >= max(map(os.path.getmtime, (BINDING, header)))):
         return
-    import torch
     from torch.utils import cpp_extension
     inc = cpp_extension.include_paths() + [sysconfig.get_paths()["include"], INCLUDE]
     cuda = os.path.join(os.path.dirname(os.path.dirname(_nvcc())), "include")

@@ -46,9 +46,9 @@ _native = None
 
 
 def _load_native(lib):
-    """The native marshalling of the layer operators' calls, or None where it is not built, or
-    was built against another torch."""
-    path = os.path.join(_HERE, "_native.so")
+    """The native marshalling of the layer operators' calls, or None where it is not built for
+    this torch."""
+    path = os.path.join(_HERE, "_native-%s.so" % torch.__version__)
     if not os.path.exists(path):
         return None
     try:

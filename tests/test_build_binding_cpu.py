@@ -50,3 +50,21 @@ def test_a_failing_library_is_an_error(elsewhere):
     fails["nvcc"] = RuntimeError("nvcc")
     with pytest.raises(RuntimeError):
         s6build.build()
+
+
+def test_another_torch_gets_a_binding_of_its_own(monkeypatch):
+    """What is up to date for one torch is not for another, and is not loaded by it."""
+    import importlib
+
+    import torch
+
+    from selective_state_space_56_b200 import ops
+    mine = s6build.BINDING_PATH
+    monkeypatch.setattr(torch, "__version__", "9.9.9")
+    try:
+        assert importlib.reload(s6build).BINDING_PATH != mine
+        assert not os.path.exists(s6build.BINDING_PATH)
+        assert ops._load_native(ops.load_library()) is None
+    finally:
+        monkeypatch.undo()
+        assert importlib.reload(s6build).BINDING_PATH == mine
