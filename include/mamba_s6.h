@@ -667,6 +667,12 @@ int mamba_diag_wait_timeout(int64_t limit_cycles, void* stream);
 int mamba_diag_wait_timeout_in(int part, int64_t limit_cycles, void* stream);
 
 /*
+ * Diagnostic: the warps of a CTA and the CTAs of a cluster that walk a row of the gated recurrence
+ * together for these sizes (1 and 1: a warp by itself).  Host only.  Errors: NULL, DIMS.
+ */
+int mamba_diag_gated_team(mamba_gated_dims dims, int backward, int* warps, int* ctas);
+
+/*
  * Diagnostic: evaluates 2^x for n floats three ways on the device -- the FMA-pipe
  * polynomial the scan uses for part of its Abar factors (out_fma), the SFU
  * ex2.approx instruction (out_sfu) and CUDA's exp2f (out_lib) -- so tests can bound

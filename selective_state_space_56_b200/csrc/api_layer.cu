@@ -61,6 +61,15 @@ size_t mamba_gated_scan_bwd_workspace_size(mamba_gated_dims dims) {
     return (size_t)bias_bytes(dims) + mamba_gated_scan_checkpoints_size(dims);
 }
 
+int mamba_diag_gated_team(mamba_gated_dims dims, int backward, int* warps, int* ctas) {
+    if (!warps || !ctas) return MAMBA_ERR_NULL;
+    if (!gated_dims_ok(dims)) return MAMBA_ERR_DIMS;
+    const s6::GatedTeam t = s6::gated_team(dims.batch * dims.dim, dims.seqlen, backward != 0);
+    *warps = t.warps;
+    *ctas = t.ctas;
+    return MAMBA_OK;
+}
+
 int mamba_gated_scan_fwd(const void* x, const void* gate, const float* gate_bias, const void* z,
                          const float* initial_state, void* y, float* last_state,
                          float* checkpoints, size_t checkpoint_bytes, mamba_gated_dims dims,

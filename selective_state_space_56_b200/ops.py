@@ -129,6 +129,8 @@ def load_library():
             for name in ("checkpoints", "bwd_workspace"):
                 fn = getattr(lib, "mamba_gated_scan_%s_size" % name)
                 fn.restype, fn.argtypes = size, [GatedDims]
+            lib.mamba_diag_gated_team.restype = i32
+            lib.mamba_diag_gated_team.argtypes = [GatedDims, i32] + [ctypes.POINTER(ctypes.c_int)] * 2
             lib.mamba_add_rms_norm_bwd_workspace_size.restype = size
             lib.mamba_add_rms_norm_bwd_workspace_size.argtypes = [i64, i64]
             for name, args in (
@@ -684,6 +686,16 @@ def _workspace(workspace, need, like, dev):
     if workspace is None and need > 0:
         workspace = _new(like, need, torch.uint8)
     return (workspace, *_buffer(workspace, "workspace", dev))
+
+
+def diag_gated_team(batch: int, dim: int, seqlen: int, backward: bool = False) -> tuple:
+    """(warps of a CTA, CTAs of a cluster) that walk a row together for these sizes."""
+    warps, ctas = ctypes.c_int(), ctypes.c_int()
+    rc = load_library().mamba_diag_gated_team(GatedDims(batch, dim, seqlen), int(bool(backward)),
+                                              ctypes.byref(warps), ctypes.byref(ctas))
+    if rc != 0:
+        raise MambaError(rc, "mamba_diag_gated_team")
+    return warps.value, ctas.value
 
 
 def gated_scan_fwd(x, gate, gate_bias=None, z=None, initial_state=None, given_decay=False,
