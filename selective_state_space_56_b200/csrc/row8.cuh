@@ -141,8 +141,9 @@ struct Quotient {
         hi = pack2(h, h);
         lo = pack2(l, l);
     }
+    static constexpr float kLargest = 3.40282347e38f;  // of fp32
     __device__ __forceinline__ static float rest(float h, float m) {
-        return fmaf(-h, fminf(m, 3e38f), kE4m3Max) * (h * (1.f / kE4m3Max));
+        return fmaf(-h, fminf(m, kLargest), kE4m3Max) * (h * (1.f / kE4m3Max));
     }
     __device__ __forceinline__ f2 operator()(f2 v) const { return fma2(v, hi, mul2(v, lo)); }
     // Eight values of a group, in place.

@@ -77,6 +77,28 @@ def test_quotients_round_to_nearest_even(cuda_ok, call):
         assert torch.equal(s.flatten().cpu(), x.float().abs().amax(1) / 448.0)
 
 
+@pytest.mark.parametrize("call", ["rows", "channels", "weight"])
+@pytest.mark.parametrize("exponent", [127, 126, 100, 0, -60, -99])
+def test_groups_of_any_magnitude(cuda_ok, call, exponent):
+    """The same groups at other powers of two: up to the largest values of bf16, down to the floor of the
+    scale's numerator (1e-30 > 2^-100)."""
+    x, want = groups()
+    x = x.double()
+    x = (x * torch.exp2(exponent - torch.floor(torch.log2(x[:, :1])))).float().bfloat16()
+    if call == "channels":
+        q, s = ops.fp8_quantize(x.t().contiguous()[None].to(DEV), channel_major=True)
+    elif call == "weight":
+        w = torch.zeros(len(x), 128, 128, dtype=torch.bfloat16)
+        w[:, 127] = x
+        q, s = ops.fp8_quantize_weight(w.view(-1, 128).to(DEV))
+        q = q.view(torch.uint8).view(-1, 128, 128)[:, 127].contiguous().view(torch.float8_e4m3fn)
+    else:
+        q, s = ops.fp8_quantize(x.to(DEV))
+    got = q.float().double().cpu().numpy()
+    assert np.array_equal(got, want), "%d values differ" % int((got != want).sum())
+    assert torch.equal(s.flatten().cpu(), x.float().abs().amax(1) / 448.0)
+
+
 def test_equal_calls_give_equal_bits(cuda_ok):
     g = torch.Generator(device=DEV).manual_seed(1)
     cm = torch.randn(2, 1536, 333, generator=g, device=DEV).bfloat16()
