@@ -276,8 +276,9 @@ __global__ void __launch_bounds__(ALONE ? 32 * kAloneWarps : kMaxThreads, ALONE 
 }
 
 // The same for any dim: a thread takes C single columns, threadIdx.x + i blockDim.x, of every
-// row, so that its share of dweight stays in registers there too; the next row's values are on
-// their way while this one is computed.  (16384, 1023) bf16: 122 us with two passes over a row
+// row, so that its share of dweight is its own there too (in registers up to C = 8; the instance of 32,
+// for widths above 4096, keeps its arrays in local memory, 1 KB a thread); the next row's values are
+// on their way while this one is computed.  (16384, 1023) bf16: 122 us with two passes over a row
 // and shares in memory, 57 so.
 template <typename Tx, typename Tr, int C>
 __global__ void __launch_bounds__(kMaxThreads) norm_bwd_elem_kernel(const BNParams p) {
