@@ -262,7 +262,9 @@ __device__ __forceinline__ int64_t cm_index(const LParams& p, int64_t t, int64_t
     return (b * p.n + n) * p.seqlen + (t - b * p.seqlen);
 }
 
+// (The aligned forms take whole warps, whatever branch some lanes come from.)
 __device__ __forceinline__ void cluster_sync() {
+    __syncwarp();
     asm volatile("barrier.cluster.arrive.aligned;\nbarrier.cluster.wait.aligned;" ::: "memory");
 }
 __device__ __forceinline__ uint32_t cluster_rank() {
@@ -532,6 +534,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ C
             const int64_t t_done = t0, n_done = n0;
             if (tile + pairs < tiles) begin(tile + pairs);  // its first scales arrive during the stores
             if (n_done < p.n && t_done < p.tokens) store_tile<Tout>(p, &mo, stage, t_done, n_done, lane, acc);
+            __syncwarp();  // the next load of tensor memory takes the whole warp
         }
         if (lane == 0) tma_store_wait_all();
     }
@@ -699,9 +702,9 @@ token_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUt
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    __syncwarp();
     if (warp == 5) tmem_free(tmem, kCols);
     const bool bad = bars.ctl.abort != 0;
-    __syncwarp();
     cluster_sync();
     if (!bad) {
         // This CTA's share of the 128 outputs of every token, four at a time.  Channel-major, the
@@ -747,6 +750,7 @@ token_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUt
     }
     // A CTA's shared memory outlives its peers' reads.  They are done (their values were used), so the
     // arrival need not wait for the outputs' way to memory as a releasing one does.
+    __syncwarp();
     asm volatile("barrier.cluster.arrive.relaxed.aligned;\nbarrier.cluster.wait.aligned;" ::: "memory");
 }
 

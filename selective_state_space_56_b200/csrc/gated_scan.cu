@@ -225,7 +225,9 @@ __device__ __forceinline__ uint32_t cluster_ctas() {
     asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
     return r;
 }
+// (The aligned forms take whole warps, whatever branch some lanes come from.)
 __device__ __forceinline__ void cluster_sync() {
+    __syncwarp();
     asm volatile("barrier.cluster.arrive.aligned;\nbarrier.cluster.wait.aligned;" ::: "memory");
 }
 // Sets up a cluster's hand-over; ends with every CTA's shared memory in place.
