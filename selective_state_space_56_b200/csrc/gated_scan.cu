@@ -860,15 +860,8 @@ cudaError_t launch_gated_timeout_probe(long long limit_cycles, cudaStream_t s) {
     return cudaGetLastError();
 }
 
-cudaError_t read_gated_error(unsigned* out, bool clear, cudaStream_t s) {
-    cudaError_t e = cudaMemcpyFromSymbolAsync(out, g_gated_error, sizeof(unsigned), 0, cudaMemcpyDeviceToHost, s);
-    if (e == cudaSuccess) e = cudaStreamSynchronize(s);
-    if (e == cudaSuccess && clear && *out) {
-        const unsigned zero = 0;
-        e = cudaMemcpyToSymbolAsync(g_gated_error, &zero, sizeof(zero), 0, cudaMemcpyHostToDevice, s);
-        if (e == cudaSuccess) e = cudaStreamSynchronize(s);
-    }
-    return e;
+cudaError_t gated_error_word(unsigned** word) {
+    return cudaGetSymbolAddress(reinterpret_cast<void**>(word), g_gated_error);
 }
 
 }  // namespace s6

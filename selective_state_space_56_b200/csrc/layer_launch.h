@@ -56,8 +56,8 @@ cudaError_t launch_gated_scan(const GatedArgs& a, cudaStream_t stream);
 // a.ckpt holds the checkpoints already.
 cudaError_t launch_gated_scan_bwd(const GatedArgs& a, const GatedBwdArgs& g, cudaStream_t stream);
 
-// Bit 0 of the recurrence's device error word (a bounded wait gave up), as read_device_error.
-cudaError_t read_gated_error(unsigned* out, bool clear, cudaStream_t stream);
+// The recurrence's error word, as device_error_word.
+cudaError_t gated_error_word(unsigned** word);
 // One wait of limit_cycles on a barrier that nothing completes; sets that word.
 cudaError_t launch_gated_timeout_probe(long long limit_cycles, cudaStream_t stream);
 
@@ -135,8 +135,8 @@ struct LinearArgs {
     DType out_dtype;
 };
 cudaError_t launch_fp8_linear(const LinearArgs& a, cudaStream_t stream);
-// Bit 0 of the projection's device error word (a bounded wait gave up), as read_device_error.
-cudaError_t read_linear_error(unsigned* out, bool clear, cudaStream_t stream);
+// The projection's error word, as device_error_word.
+cudaError_t linear_error_word(unsigned** word);
 cudaError_t launch_linear_timeout_probe(long long limit_cycles, cudaStream_t stream);  // as for the recurrence
 
 }  // namespace s6

@@ -198,8 +198,7 @@ cudaError_t launch_conv1d_bwd(const ConvBwdArgs& a, cudaStream_t stream);
 // after limit_cycles SM clocks.
 cudaError_t launch_wait_timeout_probe(long long limit_cycles, cudaStream_t stream);
 
-// Reads (and optionally clears) the device error word on `stream`, synchronising it.
-// Bit 0: a bounded device-side wait gave up.
-cudaError_t read_device_error(unsigned* out, bool clear, cudaStream_t stream);
+// Where the scans' error word lies on the current device.  Bit 0: a bounded device-side wait gave up.
+cudaError_t device_error_word(unsigned** word);
 
 }  // namespace s6

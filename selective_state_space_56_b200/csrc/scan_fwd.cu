@@ -47,7 +47,7 @@
 
 namespace s6 {
 
-// Bit 0: a bounded device wait gave up (read and cleared through read_device_error).
+// Bit 0: a bounded device wait gave up (read and cleared through device_error_word).
 __device__ unsigned int g_device_error = 0;
 
 namespace {
@@ -1421,19 +1421,8 @@ cudaError_t launch_wait_timeout_probe(long long limit_cycles, cudaStream_t strea
     return cudaGetLastError();
 }
 
-cudaError_t read_device_error(unsigned* out, bool clear, cudaStream_t stream) {
-    unsigned v = 0;
-    cudaError_t e = cudaMemcpyFromSymbolAsync(&v, g_device_error, sizeof(v), 0,
-                                              cudaMemcpyDeviceToHost, stream);
-    if (e == cudaSuccess) e = cudaStreamSynchronize(stream);
-    if (e == cudaSuccess && clear && v) {
-        const unsigned zero = 0;
-        e = cudaMemcpyToSymbolAsync(g_device_error, &zero, sizeof(zero), 0,
-                                    cudaMemcpyHostToDevice, stream);
-        if (e == cudaSuccess) e = cudaStreamSynchronize(stream);
-    }
-    *out = v;
-    return e;
+cudaError_t device_error_word(unsigned** word) {
+    return cudaGetSymbolAddress(reinterpret_cast<void**>(word), g_device_error);
 }
 
 namespace {
