@@ -505,7 +505,8 @@ size_t mamba_gated_scan_bwd_workspace_size(mamba_gated_dims dims);
  *   checkpoints   : NULL, or checkpoint_bytes >= mamba_gated_scan_checkpoints_size(dims)
  *                   bytes that receive the state entering every 256 steps, for the backward
  *
- * fp32 arithmetic and state.  Errors: NULL, DIMS, ALIGN, DTYPE, WORKSPACE, FLAGS, CUDA.
+ * fp32 arithmetic and state; s and 1 - s are each accurate relative to their own size.  Errors: NULL,
+ * DIMS, ALIGN, DTYPE, WORKSPACE, FLAGS, CUDA.
  */
 int mamba_gated_scan_fwd(const void* x, const void* gate, const float* gate_bias, const void* z,
                          const float* initial_state, void* y, float* last_state,
@@ -607,7 +608,7 @@ int mamba_add_rms_norm_bwd(const void* dout, const void* residual_out, const flo
  * mamba_add_rms_norm_fp8; NaN stays NaN, a group with an infinity has scale infinity).
  *
  *   x      : (batch * seqlen, dim) dtype, or (batch, dim, seqlen) when channel_major != 0 (the
- *            layout of the scan's y: the call also transposes)
+ *            layout of the scan's y: the call also transposes; batch <= 65535 then)
  *   q      : (batch * seqlen, dim) e4m3                dim a multiple of 16
  *   scales : (batch * seqlen, ceil(dim / 128)) float32
  *
@@ -641,11 +642,12 @@ int mamba_fp8_linear(const void* xq, const float* x_scales, const void* wq, cons
                      mamba_dtype out_dtype, void* stream);
 
 /*
- * Reads the library's device error word on `stream`, synchronising that stream.
+ * Reads the library's device error words (the scans', the projection's, the gated recurrence's)
+ * on `stream`, synchronising that stream.
  * Every device-side wait in the kernels (on the completion barrier of an
  * asynchronous tile copy) is bounded to about a second; a wait that gives up sets
- * the word and its CTA stops instead of hanging the GPU.  With `clear` nonzero the
- * word is reset.  Returns MAMBA_OK, MAMBA_ERR_TIMEOUT if a wait gave up since the
+ * its word and its CTA stops instead of hanging the GPU.  With `clear` nonzero the
+ * words are reset once they have been read.  Returns MAMBA_OK, MAMBA_ERR_TIMEOUT if a wait gave up since the
  * last clear (outputs of that call are then undefined), or MAMBA_ERR_CUDA.
  */
 int mamba_check_device_error(int clear, void* stream);

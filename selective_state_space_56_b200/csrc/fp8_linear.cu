@@ -14,8 +14,10 @@
 //                    CTAs (cta_group::2): each loads half of either operand, which halves the
 //                    weights' share of the shared-memory traffic that a 128 x 256 tile of one CTA is
 //                    bound by.  A lane is a token, so its scale is one register a block.
-//                    16384 tokens, 2560 -> 10240: 391 us, 2.2 PFLOP/s, the tensor pipe 52% busy;
-//                    bound by the summing warps' reads of tensor memory.
+//                    16384 tokens, 2560 -> 10240: 388 us back to back on the device, 2.2 PFLOP/s, the
+//                    tensor pipe 52% busy (a pass behind a flush of L2 455-463 us); bound by the
+//                    summing warps (without their multiply-adds 334 us, without their reads of
+//                    tensor memory alone no less) and the hand-overs to and from them.
 //   token_kernel     few tokens: bound by the weights' bytes.  128 outputs are the MMA's rows,
 //                    the tokens its columns (16 to 64), and the inputs are cut into pieces over a
 //                    cluster whose CTAs add their sums through distributed shared memory in

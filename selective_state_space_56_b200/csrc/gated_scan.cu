@@ -138,7 +138,8 @@ __device__ __forceinline__ void set(void* p, int64_t e, const Row& w, bool edge,
 
 // Whether a warp's coming chunks wait in shared memory (a Ring) or, the next one, in registers.
 // The ring keeps more bytes in flight in fewer registers: a warp per row, (4, 5120, 4096) bf16 with
-// z 113 -> 105 us forward, 326 -> 293 with the backward, (1, 2300, 8192) 44 -> 31.  Teams have
+// z 113 -> 105 us forward on the device, 326 -> 293 with the backward, (1, 2300, 8192) 44 -> 31 (these
+// and the next before gate2 kept both sigmoids whole, which added 2%).  Teams have
 // their bytes in flight in many warps, and the way through shared memory lengthens their rounds
 // ((1, 60, 524287): fp32 decays 68 -> 75 us, bf16 with z and the backward 197 -> 215), except
 // where the registers do not hold a second chunk: fp32 with z (147 -> 91 forward, 352 -> 307 with
