@@ -78,7 +78,8 @@ __device__ __forceinline__ void decays(const Raw8<T>& g, float nbias, float (&a)
 #pragma unroll
     for (int i = 0; i < kE / 2; ++i) {
         if (DECAY) unpack2(g.pair(i), a[2 * i], a[2 * i + 1]);
-        else unpack2(gate2(fma2(g.pair(i), twice(-kLog2e), twice(nbias)), a[2 * i], a[2 * i + 1]), sg[2 * i], sg[2 * i + 1]);
+        else unpack2(gate2(fma2(g.pair(i), twice(-kLog2e), twice(nbias)), a[2 * i], a[2 * i + 1]),
+                     sg[2 * i], sg[2 * i + 1]);
     }
 }
 // Its inputs b_j.
@@ -534,7 +535,9 @@ __global__ void __launch_bounds__(TEAM ? 32 * kTeamWarps : 32 * kWarps, TEAM ? 1
         if (lane == 31) ev = in;
         if (!TEAM) ec = __shfl_sync(kFull, after, 0);
         if (TEAM && c >= chunks) continue;
-        float b[kE], hv[kE];  // inputs (formed here, so that the sigmoids alone wait for the gradients), states before each step
+        // the inputs, formed here so that the sigmoids alone wait for the gradients, and the states before
+        // each step
+        float b[kE], hv[kE];
         inputs<DECAY>(xr, sg, b);
         if (edge) outside(e, w, b, 0.f);
         {
